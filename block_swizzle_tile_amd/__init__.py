@@ -11,6 +11,9 @@ Names follow the C ABI without the ``bst_`` prefix: :func:`gemm`,
 :func:`batched_gemm`, :func:`grouped_gemm_slice_m`, :func:`grouped_gemm_slice_k`,
 :func:`quant_gemm_per_token`, :func:`tile_map`, :func:`grouped_tile_map`,
 :func:`workspace_bytes`, :func:`effective_sched`.
+
+The block-scaled 8-bit operators (``include/bst_block.h``: quantise, restore, products, weight
+gradients) are in :mod:`.block` and reached from here by the same names.
 """
 from __future__ import annotations
 
@@ -25,7 +28,21 @@ _DIRS = {"zn": ZN, "nz": NZ, "raster": RASTER}
 __all__ = ["Sched", "BstError", "make_sched", "gemm", "gemm_padded", "batched_gemm",
            "grouped_gemm_slice_m", "grouped_gemm_slice_k",
            "quant_gemm_per_token", "tile_map", "grouped_tile_map", "workspace_bytes",
-           "effective_sched", "task_count", "clock_record", "version", "LIB_PATH"]
+           "effective_sched", "task_count", "clock_record", "version", "LIB_PATH",
+           "quant_block", "dequant_block", "gemm_block_scaled", "grouped_gemm_block_scaled",
+           "weight_grad", "grouped_weight_grad", "block_workspace_bytes"]
+
+# the block-scaled operators' binding imports torch: on first use, like the rest of the package
+_BLOCK = {"quant_block", "dequant_block", "gemm_block_scaled", "grouped_gemm_block_scaled",
+          "weight_grad", "grouped_weight_grad", "block_workspace_bytes"}
+
+
+def __getattr__(name):
+    if name in _BLOCK:
+        from . import block
+        globals().update({n: getattr(block, n) for n in _BLOCK})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 def make_sched(tile=(0, 0), tile_k=0, offset=1, direction="zn", split_k=1, xcd_remap=0, grid=0,

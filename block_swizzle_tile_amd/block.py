@@ -1,0 +1,333 @@
+"""Block-scaled 8-bit operators: the binding of ``include/bst_block.h``.
+
+An 8-bit matrix is a pair (codes, scales): ``torch.float8_e4m3fn`` codes with one scale per 128
+values of a row (activations, scales ``[M][ceil(K/128)]``) or per 128 x 128 square (weights).
+Scales are E8M0 bytes (``torch.uint8`` or ``torch.float8_e8m0fnu``) or ``torch.float32``.
+
+One linear layer, y = x @ w, in 8 bits::
+
+    xq, xs = quant_block(x)                            # kept for the backward pass
+    wq, ws = quant_block(w, block_rows=128)
+    y = gemm_block_scaled(xq, wq, xs, ws)
+    dyq, dys = quant_block(dy)
+    dx = gemm_block_scaled(dyq, wq, dys, ws, trans_b=True)    # dy @ w.T
+    dw = weight_grad(xq, xs, dy)                       # x.T @ dy, from the 8-bit x
+
+As in the rest of the package the functions only check and pass arguments; the work runs on the
+current stream of the operands' device.  Outputs and workspaces come from torch's allocator in
+that stream's order, so calls on several streams, and captured calls, never share one unless the
+caller passes it.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+
+from ._lib import BF16, F16, F32, Sched, check, lib
+
+E8M0 = 8
+
+BLOCK_EXPORTS = ["bst_quant_block", "bst_dequant_block", "bst_gemm_block_scaled",
+                 "bst_grouped_gemm_block_scaled", "bst_weight_grad", "bst_grouped_weight_grad",
+                 "bst_block_workspace_bytes"]
+
+_KIND = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+_SCALE = {torch.float32: F32, torch.uint8: E8M0, torch.float8_e8m0fnu: E8M0}
+_CODES = torch.float8_e4m3fn
+
+
+@functools.lru_cache(maxsize=None)
+def _bound():
+    L = lib()
+    i64, i32, p, st = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int
+    sz, sp = ctypes.c_size_t, ctypes.POINTER(Sched)
+    L.bst_quant_block.argtypes = [st, i64, i64, i32, p, i64, p, i64, p, i64, p]
+    L.bst_dequant_block.argtypes = [st, i64, i64, i32, p, i64, st, p, i64, p, i64, p]
+    L.bst_gemm_block_scaled.argtypes = [st, i32, i64, i64, i64, p, i64, st, p, i64, p, i64, st, p,
+                                        i64, p, i64, sp, p, sz, p]
+    L.bst_grouped_gemm_block_scaled.argtypes = [st, i32, i32, p, i64, i64, i64, p, i64, st, p, i64,
+                                                p, i64, i64, st, p, i64, i64, p, i64, sp, p]
+    L.bst_weight_grad.argtypes = [st, st, i64, i64, i64, p, i64, p, i64, p, i64, p, i64, p, i64,
+                                  sp, p, sz, p]
+    L.bst_grouped_weight_grad.argtypes = [st, st, i32, p, i64, i64, i64, p, i64, p, i64, p, i64, p,
+                                          i64, i64, p, i64, i64, sp, p, sz, p]
+    for n in BLOCK_EXPORTS[:-1]:
+        getattr(L, n).restype = st
+    L.bst_block_workspace_bytes.argtypes = [st, i64, i64, i64, i64, sp]
+    L.bst_block_workspace_bytes.restype = sz
+    return L
+
+
+def _cdiv(a, b):
+    return -(-a // b)
+
+
+def _kind(t, what):
+    k = _KIND.get(t)
+    if k is None:
+        raise TypeError("%s: unsupported dtype %s" % (what, t))
+    return k
+
+
+def _mat(t, what, shape, dims=2, pad=1):
+    """Pitch of a row-major matrix (or of each of a stack); one row has any pitch, so the least
+    legal one (a multiple of pad) is given for it."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
+    cols = shape[-1]
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError("%s: innermost dimension must be contiguous" % what)
+    if shape[-2] <= 1:
+        return _cdiv(cols, pad) * pad
+    return t.stride(-2)
+
+
+def _codes(t, what):
+    if t.dtype != _CODES:
+        raise TypeError("%s: expected float8_e4m3fn codes, got %s" % (what, t.dtype))
+
+
+def _scale_kind(t, what):
+    k = _SCALE.get(t.dtype)
+    if k is None:
+        raise TypeError("%s: scales are uint8 / float8_e8m0fnu (E8M0) or float32, not %s" %
+                        (what, t.dtype))
+    return k
+
+
+def _device(first, *rest):
+    d = first.device
+    if d.type != "cuda":
+        raise ValueError("operands must be GPU tensors")
+    for t in rest:
+        if t is not None and t.device != d:
+            raise ValueError("operands are on different devices (%s, %s)" % (d, t.device))
+    return d
+
+
+def _guard(fn):
+    """Runs fn with its first tensor's device current: kernels launch on the current device."""
+    @functools.wraps(fn)
+    def call(first, *args, **kwargs):
+        d = first.device
+        if d.type == "cuda" and d.index != torch.cuda.current_device():
+            with torch.cuda.device(d):
+                return fn(first, *args, **kwargs)
+        return fn(first, *args, **kwargs)
+    return call
+
+
+def _stream(d):
+    return torch.cuda.current_stream(d).cuda_stream
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _s(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def block_workspace_bytes(kind, count, M, N, K, sched=None):
+    """Workspace bytes of :func:`gemm_block_scaled` (kind 0), :func:`weight_grad` (1) or
+    :func:`grouped_weight_grad` (2, count = groups, M = rows in all) on the current device."""
+    return _bound().bst_block_workspace_bytes(kind, count, M, N, K, _s(sched))
+
+
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(device, kind, count, M, N, K):
+    return block_workspace_bytes(kind, count, M, N, K)
+
+
+def _workspace(ws, d, kind, count, M, N, K, sched):
+    if ws is not None:
+        if ws.device != d:
+            raise ValueError("the workspace is on another device")
+        if not ws.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
+        return ws, ws.numel() * ws.element_size()
+    n = (_ws_bytes(d.index, kind, count, M, N, K) if sched is None
+         else block_workspace_bytes(kind, count, M, N, K, sched))
+    if n == 0:
+        return None, 0
+    return torch.empty(n, dtype=torch.uint8, device=d), n
+
+
+@_guard
+def quant_block(X, Q=None, scale=None, *, block_rows=1):
+    """8-bit codes and E8M0 scales of X [M][K] (bf16, fp16 or fp32): (Q, scale).
+
+    block_rows: 1 for one scale per 128 values of a row (activations), 128 for 128 x 128 squares
+    (weights).  A new Q has rows of whole 16-byte chunks, as the products take them, so for K %
+    16 != 0 it is a view of a wider matrix.  Rounding is to nearest even under the smallest
+    power-of-two scale that holds the block's largest finite magnitude; infinities and NaN become
+    NaN (bst_quant_block)."""
+    if X.dim() != 2:
+        raise ValueError("X must be a matrix")
+    M, K = X.shape
+    kind = _kind(X.dtype, "X")
+    d = _device(X, Q, scale)
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    ldx = _mat(X, "X", (M, K))
+    if Q is None:
+        if K % 16 == 0:
+            Q = torch.empty((M, K), dtype=_CODES, device=d)
+        else:
+            Q = torch.empty((M, _cdiv(K, 16) * 16), dtype=_CODES, device=d)[:, :K]
+    else:
+        _codes(Q, "Q")
+    sshape = (M if block_rows == 1 else _cdiv(M, 128), _cdiv(K, 128))
+    if scale is None:
+        scale = torch.empty(sshape, dtype=torch.uint8, device=d)
+    elif _scale_kind(scale, "scale") != E8M0:
+        raise TypeError("quant_block writes E8M0 scales")
+    check(_bound().bst_quant_block(kind, M, K, block_rows, X.data_ptr(), ldx, Q.data_ptr(),
+                                   _mat(Q, "Q", (M, K)), scale.data_ptr(),
+                                   _mat(scale, "scale", sshape), _stream(d)))
+    return Q, scale
+
+
+@_guard
+def dequant_block(Q, scale, X=None, *, out_dtype=None, block_rows=1):
+    """The matrix that codes Q and scales stand for, in out_dtype (bf16 by default; bf16, fp16 or
+    fp32); finite values past the type's range give its largest (bst_dequant_block)."""
+    _codes(Q, "Q")
+    if Q.dim() != 2:
+        raise ValueError("Q must be a matrix")
+    M, K = Q.shape
+    d = _device(Q, scale, X)
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    sk = _scale_kind(scale, "scale")
+    if X is None:
+        X = torch.empty((M, K), dtype=out_dtype or torch.bfloat16, device=d)
+    sshape = (M if block_rows == 1 else _cdiv(M, 128), _cdiv(K, 128))
+    check(_bound().bst_dequant_block(_kind(X.dtype, "X"), M, K, block_rows, Q.data_ptr(),
+                                     _mat(Q, "Q", (M, K)), sk, scale.data_ptr(),
+                                     _mat(scale, "scale", sshape), X.data_ptr(),
+                                     _mat(X, "X", (M, K)), _stream(d)))
+    return X
+
+
+def _product(A, B, scale_a, scale_b, trans_b, lead):
+    _codes(A, "A")
+    _codes(B, "B")
+    if A.dim() != 2 or B.dim() != 2 + len(lead):
+        raise ValueError("A must be a matrix, B %s" % ("a stack of matrices" if lead else "a matrix"))
+    M, K = A.shape
+    N = B.shape[-2] if trans_b else B.shape[-1]
+    kb, nb = _cdiv(K, 128), _cdiv(N, 128)
+    lda = _mat(A, "A", (M, K), pad=16)
+    ldb = _mat(B, "B", (*lead, N, K) if trans_b else (*lead, K, N), pad=16)
+    ldsa = _mat(scale_a, "scale_a", (M, kb))
+    ldsb = _mat(scale_b, "scale_b", (*lead, nb, kb) if trans_b else (*lead, kb, nb))
+    return (M, N, K, lda, ldb, ldsa, ldsb, _scale_kind(scale_a, "scale_a"),
+            _scale_kind(scale_b, "scale_b"))
+
+
+@_guard
+def gemm_block_scaled(A, B, scale_a, scale_b, C=None, *, trans_b=False, out_dtype=None, sched=None,
+                      workspace=None):
+    """C = A @ B of two 8-bit matrices with block scales (fp32 sums; bf16 out by default).
+
+    A [M][K] with scale_a [M][ceil(K/128)]; B [K][N] with scale_b [ceil(K/128)][ceil(N/128)], or
+    with trans_b B [N][K] and scale_b [ceil(N/128)][ceil(K/128)] (bst_gemm_block_scaled)."""
+    trans_b = bool(trans_b)
+    d = _device(A, B, scale_a, scale_b, C)
+    M, N, K, lda, ldb, ldsa, ldsb, ka, kb = _product(A, B, scale_a, scale_b, trans_b, ())
+    if C is None:
+        C = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=d)
+    ws, wsb = _workspace(workspace, d, 0, 1, M, N, K, sched)
+    check(_bound().bst_gemm_block_scaled(_kind(C.dtype, "C"), trans_b, M, N, K, A.data_ptr(), lda,
+                                         ka, scale_a.data_ptr(), ldsa, B.data_ptr(), ldb, kb,
+                                         scale_b.data_ptr(), ldsb, C.data_ptr(),
+                                         _mat(C, "C", (M, N)), _s(sched), _p(ws), wsb, _stream(d)))
+    return C
+
+
+def _groups(group_m):
+    if group_m.dtype != torch.int32 or group_m.dim() != 1 or not group_m.is_contiguous():
+        raise TypeError("group_m must be a contiguous int32 vector")
+    return group_m.numel()
+
+
+@_guard
+def grouped_gemm_block_scaled(A, B, group_m, scale_a, scale_b, C=None, *, trans_b=False,
+                              out_dtype=None, sched=None):
+    """Groups of rows stacked along M, each times its own B[g]: group_m is a device int32 vector of
+    row counts (never read on the host).  Rows of C past the last group are left as they were
+    (unset in a new C) (bst_grouped_gemm_block_scaled)."""
+    trans_b = bool(trans_b)
+    d = _device(A, B, group_m, scale_a, scale_b, C)
+    G = _groups(group_m)
+    M, N, K, lda, ldb, ldsa, ldsb, ka, kb = _product(A, B, scale_a, scale_b, trans_b, (G,))
+    if C is None:
+        C = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=d)
+    check(_bound().bst_grouped_gemm_block_scaled(
+        _kind(C.dtype, "C"), trans_b, G, group_m.data_ptr(), M, N, K, A.data_ptr(), lda, ka,
+        scale_a.data_ptr(), ldsa, B.data_ptr(), ldb, B.stride(0) if G > 1 else 0, kb,
+        scale_b.data_ptr(), ldsb, scale_b.stride(0) if G > 1 else 0, C.data_ptr(),
+        _mat(C, "C", (M, N)), _s(sched), _stream(d)))
+    return C
+
+
+def _grad_out(dW, add, out_dtype, shape, d):
+    if dW is None:
+        dtype = out_dtype or (add.dtype if add is not None else torch.float32)
+        dW = torch.empty(shape, dtype=dtype, device=d)
+    if add is not None and add.dtype != dW.dtype:
+        raise TypeError("add must have dW's dtype")
+    return dW
+
+
+def _grad_in(Q, scale, dY):
+    _codes(Q, "Q")
+    if Q.dim() != 2 or dY.dim() != 2:
+        raise ValueError("Q and dY must be matrices")
+    if _scale_kind(scale, "scale") != E8M0:
+        raise TypeError("activations kept in 8 bits have E8M0 scales (quant_block)")
+    M, K = Q.shape
+    N = dY.shape[1]
+    return (M, K, N, _mat(Q, "Q", (M, K), pad=16), _mat(scale, "scale", (M, _cdiv(K, 128))),
+            _mat(dY, "dY", (M, N)))
+
+
+@_guard
+def weight_grad(Q, scale, dY, dW=None, *, add=None, out_dtype=None, sched=None, workspace=None):
+    """dW [K][N] = add + X.T @ dY for X [M][K] kept in 8 bits as quant_block made it (codes Q, E8M0
+    scales) and dY [M][N] in bf16, fp16 or fp32; no operand is rounded, sums are fp32.  add: dW's
+    dtype and shape, may be dW itself (gradient accumulation).  fp32 out by default
+    (bst_weight_grad)."""
+    d = _device(Q, scale, dY, dW, add)
+    M, K, N, ldq, lds, ldy = _grad_in(Q, scale, dY)
+    dW = _grad_out(dW, add, out_dtype, (K, N), d)
+    ws, wsb = _workspace(workspace, d, 1, 1, M, N, K, sched)
+    check(_bound().bst_weight_grad(
+        _kind(dY.dtype, "dY"), _kind(dW.dtype, "dW"), M, N, K, Q.data_ptr(), ldq, scale.data_ptr(),
+        lds, dY.data_ptr(), ldy, _p(add), _mat(add, "add", (K, N)) if add is not None else 0,
+        dW.data_ptr(), _mat(dW, "dW", (K, N)), _s(sched), _p(ws), wsb, _stream(d)))
+    return dW
+
+
+@_guard
+def grouped_weight_grad(Q, scale, dY, group_m, dW=None, *, add=None, out_dtype=None, sched=None,
+                        workspace=None):
+    """weight_grad over each group of rows: dW [G][K][N], group_m a device int32 vector of row
+    counts; an empty group's gradient is its add (or zeros) (bst_grouped_weight_grad)."""
+    d = _device(Q, scale, dY, group_m, dW, add)
+    G = _groups(group_m)
+    M, K, N, ldq, lds, ldy = _grad_in(Q, scale, dY)
+    dW = _grad_out(dW, add, out_dtype, (G, K, N), d)
+    lda = _mat(add, "add", (G, K, N)) if add is not None else 0
+    ws, wsb = _workspace(workspace, d, 2, G, M, N, K, sched)
+    check(_bound().bst_grouped_weight_grad(
+        _kind(dY.dtype, "dY"), _kind(dW.dtype, "dW"), G, group_m.data_ptr(), M, N, K, Q.data_ptr(),
+        ldq, scale.data_ptr(), lds, dY.data_ptr(), ldy, _p(add), lda,
+        add.stride(0) if add is not None and G > 1 else 0, dW.data_ptr(),
+        _mat(dW, "dW", (G, K, N)), dW.stride(0) if G > 1 else 0, _s(sched), _p(ws), wsb,
+        _stream(d)))
+    return dW

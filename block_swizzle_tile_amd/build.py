@@ -9,10 +9,14 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["bst.hip", "inst_f16.hip", "inst_bf16.hip", "inst_i8.hip", "inst_fp8.hip",
-           "inst_mxfp8.hip", "inst_slicek.hip"]
-HEADERS = ["bst_device.hpp", "bst_kernel_dma.hpp", "bst_instances.hpp"]
+           "inst_mxfp8.hip", "inst_slicek.hip", "block.hip", "block_gemm_plain_t.hip",
+           "block_gemm_plain_n.hip", "block_gemm_grouped_t.hip", "block_gemm_grouped_n.hip",
+           "block_grad.hip"]
+HEADERS = ["bst_device.hpp", "bst_kernel_dma.hpp", "bst_instances.hpp", "bst_block.hpp",
+           "bst_block_gemm.hpp", "bst_block_grad.hpp", "bst_block_quant.hpp",
+           "bst_block_instances.hpp"]
 DEPS = ([os.path.join(CSRC, f) for f in SOURCES + HEADERS] +
-        [os.path.join(ROOT, "include", "bst.h")])
+        [os.path.join(ROOT, "include", f) for f in ("bst.h", "bst_block.h")])
 LIB = os.path.join(PKG, "libbst.so")
 # The same kernels with cycle accounting (-DBST_TRACE): per-wave K-loop and
 # task phase cycles of workgroup 0 and a per-workgroup shader-clock record,

@@ -553,6 +553,19 @@ bst_status scratch_ptr(void* stream, void** out) {
 
 }  // namespace
 
+// What the library's other host code shares: this thread's error message and
+// the CU count.
+namespace bst {
+bst_status set_error(bst_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return st;
+}
+int device_cu_count() { return device_cus(); }
+}  // namespace bst
+
 extern "C" {
 
 #ifdef BST_TRACE

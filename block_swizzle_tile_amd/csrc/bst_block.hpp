@@ -1,0 +1,250 @@
+// bst_block.hpp -- what the block-scaled 8-bit operators share on the device:
+// scale decoding, group tables, the masked row stores of an output tile, and
+// the fixed-order sum of split partials.
+#pragma once
+
+#include "bst.h"
+#include "bst_block.h"
+#include "bst_kernel_dma.hpp"
+
+namespace bst {
+
+// Defined with the C ABI's other host code: records the message that
+// bst_last_error() returns on this thread, and passes the status through.
+bst_status set_error(bst_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int device_cu_count();
+
+constexpr uint32_t kScaleBlock = 128;  // values that share a scale
+
+enum ScaleKind { SCALE_E8M0 = 8, SCALE_F32 = 7 };
+
+// 2^(e - 127); byte 0 is the subnormal 2^-127, byte 255 NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t e) {
+  const uint32_t bits = e == 0u ? 0x00400000u : e == 255u ? 0x7fc00000u : e << 23;
+  return __builtin_bit_cast(float, bits);
+}
+
+// A wave-uniform scale through the scalar cache: a byte is cut out of the
+// aligned dword that holds it (which never leaves the byte's page), so that
+// no vector load joins the DMA instructions counted in vmcnt.
+__device__ __forceinline__ uint32_t scalar_dword(const uint8_t* p) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  const uint64_t u = ((uint64_t)hi << 32) | lo;
+  const uint32_t w = *(const __attribute__((address_space(4))) uint32_t*)(u & ~(uint64_t)3);
+  return w >> (8u * (lo & 3u));
+}
+
+// Groups of stacked rows, in LDS: each group's first task and first row, and
+// the totals behind the last.
+struct RowGroups {
+  uint32_t first_task[kMaxGroups + 1];
+  uint32_t first_row[kMaxGroups + 1];
+};
+
+// Built by wave 0 with a scan over the groups (lane l holds groups l*per ..):
+// sizes below 0 count as 0, and a running sum past total_m is cut to it.
+// bm, loops_n: rows per tile-row and tasks per tile-row.
+__device__ inline void build_row_groups(RowGroups& t, const int32_t* group_m, uint32_t G,
+                                        uint32_t total_m, uint32_t bm, uint32_t loops_n) {
+  if (threadIdx.x < 64u) {
+    const uint32_t lane = threadIdx.x, per = (G + 63u) / 64u;
+    const uint32_t g0 = lane * per < G ? lane * per : G, g1 = g0 + per < G ? g0 + per : G;
+    int64_t rows = 0;
+    for (uint32_t g = g0; g < g1; ++g) rows += group_m[g] > 0 ? group_m[g] : 0;
+    int64_t sum = rows;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t o = __shfl_up((long long)sum, d);
+      if ((int)lane >= d) sum += o;
+    }
+    int64_t at = sum - rows;  // rows before this lane's groups, not yet cut
+    uint32_t tasks = 0;
+    for (uint32_t g = g0; g < g1; ++g) {
+      const uint32_t lo = at < (int64_t)total_m ? (uint32_t)at : total_m;
+      at += group_m[g] > 0 ? group_m[g] : 0;
+      const uint32_t hi = at < (int64_t)total_m ? (uint32_t)at : total_m;
+      t.first_row[g] = lo;
+      t.first_task[g] = tasks;
+      tasks += (hi - lo + bm - 1) / bm * loops_n;
+      if (g + 1 == G) t.first_row[G] = hi;
+    }
+    uint32_t ts = tasks;
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = (uint32_t)__shfl_up((int)ts, d);
+      if ((int)lane >= d) ts += o;
+    }
+    const uint32_t base = ts - tasks;
+    for (uint32_t g = g0; g < g1; ++g) t.first_task[g] += base;
+    if (lane == 63u) t.first_task[G] = ts;
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------ output ------
+__device__ __forceinline__ uint32_t pack2(float a, float b, uint32_t kind) {
+  if (kind == OUT_BF16) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    b2 v;
+    v[0] = (__bf16)a;
+    v[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, v);
+  }
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  h2 v;
+  v[0] = (_Float16)a;
+  v[1] = (_Float16)b;
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ float out_value(const uint8_t* p, uint32_t kind) {
+  if (kind == OUT_F32) return *(const float*)p;
+  if (kind == OUT_BF16) return __builtin_bit_cast(float, (uint32_t)(*(const uint16_t*)p) << 16);
+  return (float)*(const _Float16*)p;
+}
+
+__device__ __forceinline__ void put_value(uint8_t* p, float v, uint32_t kind) {
+  if (kind == OUT_F32)
+    *(float*)p = v;
+  else
+    *(uint16_t*)p = (uint16_t)pack2(v, 0.0f, kind);
+}
+
+// N consecutive outputs (N = 4 or 8): with `add` the addend joins in fp32
+// before the one rounding.  whole: all N are inside the row and both rows are
+// aligned for vector access; otherwise `live` of them go one by one.
+template <int N>
+__device__ __forceinline__ void put_run(uint8_t* dst, const uint8_t* add, float (&v)[N],
+                                        uint32_t live, bool whole, uint32_t kind) {
+  const uint32_t es = kind == OUT_F32 ? 4u : 2u;
+  if (whole) {
+    if (kind == OUT_F32) {
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) {
+        f32x4_t o = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        if (add != nullptr) o += ((const f32x4_t*)add)[q];
+        ((f32x4_t*)dst)[q] = o;
+      }
+    } else {
+      uint32_t a[N / 2], o[N / 2];
+      if (add != nullptr) {
+        if constexpr (N == 8) {
+          const u32x4_t w = *(const u32x4_t*)add;
+          a[0] = w[0]; a[1] = w[1]; a[2] = w[2]; a[3] = w[3];
+        } else {
+          const u32x2_t w = *(const u32x2_t*)add;
+          a[0] = w[0]; a[1] = w[1];
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const uint16_t h = (uint16_t)(a[e / 2] >> (16 * (e & 1)));
+          v[e] += out_value((const uint8_t*)&h, kind);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1], kind);
+      if constexpr (N == 8)
+        *(u32x4_t*)dst = u32x4_t{o[0], o[1], o[2], o[3]};
+      else
+        *(u32x2_t*)dst = u32x2_t{o[0], o[1]};
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if ((uint32_t)e < live)
+      put_value(dst + e * es, v[e] + (add != nullptr ? out_value(add + e * es, kind) : 0.0f), kind);
+}
+
+// Where a tile goes: the final matrix, or a slice's partial sums (fp32, rows
+// of `ld` elements).
+struct OutTile {
+  uint8_t* dst;        // the tile's first element
+  const uint8_t* add;  // the addend's, or null
+  int64_t ld_bytes, ldadd_bytes;
+  uint32_t rows, cols;  // valid rows and columns of the tile
+  uint32_t kind;
+  bool vec;  // rows of dst (and add) start on 16-byte boundaries
+};
+
+// Stores a wave's TM x TN sub-tile held as 32x32 accumulators (lane l: row
+// l & 31 of the fragment, columns 8q + 4(l >> 5) + 0..3), one 32-row strip at
+// a time through the wave's own LDS strip, so that global stores are runs of
+// a row.  Waves do not wait for each other: LDS accesses of one wave complete
+// in order.  Strip rows are padded by 4 floats: the 32 rows' quads then fall
+// on different banks.
+template <int TN>
+struct Strip {
+  static constexpr int PITCH = TN + 4;  // floats
+  static constexpr int BYTES = 32 * PITCH * 4;
+};
+
+template <int FM, int FN>
+__device__ __forceinline__ void store_wave_tile(lds_t* strip, f32x16_t (&acc)[FM][FN], uint32_t m0,
+                                                uint32_t n0, const OutTile& o) {
+  constexpr int TN = FN * 32, P = Strip<TN>::PITCH;
+  constexpr int CPR = TN / 8;        // runs of 8 columns per row
+  constexpr int RPI = 64 / CPR;      // rows one pass of the wave stores
+  typedef __attribute__((address_space(3))) f32x4_t lds_f4_t;
+  const uint32_t lane = threadIdx.x & 63u, r = lane & 31u, hi = lane >> 5;
+  const uint32_t es = o.kind == OUT_F32 ? 4u : 2u;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    if (m0 + i * 32 >= o.rows) return;  // wave-uniform
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(lds_f4_t*)(strip + (r * P + j * 32 + 8 * q + 4 * hi) * 4) =
+            f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                    acc[i][j][4 * q + 3]};
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int s = 0; s < 32 / RPI; ++s) {
+      const uint32_t row = s * RPI + lane / CPR, c = (lane % CPR) * 8;
+      const f32x4_t a = *(const lds_f4_t*)(strip + (row * P + c) * 4);
+      const f32x4_t b = *(const lds_f4_t*)(strip + (row * P + c + 4) * 4);
+      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      const uint32_t m = m0 + i * 32 + row, n = n0 + c;
+      if (m < o.rows && n < o.cols) {
+        uint8_t* d = o.dst + (int64_t)m * o.ld_bytes + (int64_t)n * es;
+        const uint8_t* ad = o.add ? o.add + (int64_t)m * o.ldadd_bytes + (int64_t)n * es : nullptr;
+        put_run<8>(d, ad, v, o.cols - n, o.vec && o.cols - n >= 8u, o.kind);
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+}
+
+// Sum of the split partials in slice order, the addend, and the one rounding.
+// part: [split][count][rows][pitch] fp32, pitch a multiple of 4.
+struct ReduceArgs {
+  const float* part;
+  uint8_t* dst;
+  const uint8_t* add;
+  int64_t ld, stride, ldadd, strideadd;  // elements
+  uint32_t split, count, rows, cols, pitch;
+  uint32_t kind, vec;
+  FastDiv quads, by_rows;  // pitch / 4, rows
+  uint32_t total;          // count * rows * pitch / 4
+};
+
+static __global__ void __launch_bounds__(256) sum_partials(ReduceArgs a) {
+  const uint32_t es = a.kind == OUT_F32 ? 4u : 2u;
+  const int64_t slice = (int64_t)a.total * 4;
+  for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < a.total; i += gridDim.x * 256u) {
+    const uint32_t rr = a.quads.div(i), q = i - rr * a.quads.d;
+    const uint32_t g = a.by_rows.div(rr), r = rr - g * a.rows;
+    const float* p = a.part + (int64_t)i * 4;
+    f32x4_t s = *(const f32x4_t*)p;
+    for (uint32_t k = 1; k < a.split; ++k) s += *(const f32x4_t*)(p + k * slice);
+    const uint32_t n = q * 4;
+    if (n >= a.cols) continue;
+    float v[4] = {s[0], s[1], s[2], s[3]};
+    uint8_t* d = a.dst + (g * a.stride + r * a.ld + n) * es;
+    const uint8_t* ad = a.add ? a.add + (g * a.strideadd + r * a.ldadd + n) * es : nullptr;
+    put_run<4>(d, ad, v, a.cols - n, a.vec && a.cols - n >= 4u, a.kind);
+  }
+}
+
+}  // namespace bst

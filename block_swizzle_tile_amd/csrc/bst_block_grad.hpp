@@ -1,0 +1,322 @@
+// bst_block_grad.hpp -- the gradient of a linear layer's weight from its
+// input kept in 8 bits:
+//   dW[k][n] = add[k][n] + sum_m x[m][k] dY[m][n],  x[m][k] = q[m][k] 2^e[m][k/128].
+//
+// The sum runs over rows, and every row has its own scales, so they cannot
+// leave the sum: x is restored on its way into LDS.  A code times a power of
+// two is exact in bf16 (4 significant bits of 8), one conversion instruction
+// makes two of them, and each is made once per workgroup.  dY joins as bf16:
+// as it is, or as 2 (fp16) or 3 (fp32) bf16 parts that add up to it, each
+// with its own matrix product, so that nothing is rounded before the fp32
+// sums.  Both operands lie in LDS row by row (m); the transposing reads turn
+// 8 rows of a column into an operand of the 32x32x16 bf16 instruction.
+//
+// Global loads of stage s+1 are in registers while stage s is multiplied, and
+// are converted and written to the other LDS buffer behind it.
+#pragma once
+
+#include "bst_block.hpp"
+
+namespace bst {
+
+struct BlockGradArgs {
+  const uint8_t* Q;
+  const uint8_t* S;
+  const uint8_t* dY;
+  const uint8_t* add;
+  uint8_t* dW;
+  int64_t ldq, lds, lddy, ldadd, lddw;  // elements
+  int64_t strideadd, stridedw;
+  const int32_t* group_m;               // null: one group of M rows
+  float* part;                          // split > 1: [split][G][K][pitch]
+  uint32_t pitch;
+  uint32_t G, M, N, K;
+  uint32_t tiles, tiles_all;            // per group, and G times that
+  uint32_t split, remap, grid;
+  uint32_t dwkind, dwvec, dyvec;
+  MapConsts mc;                         // of one group's K x N tiles; core = tiles
+};
+
+enum DyKind { DY_BF16 = 0, DY_F16 = 1, DY_F32 = 2 };
+
+// The bf16 part of f: f cut to bf16 (toward zero, so that no finite value
+// becomes infinite); f then holds the rest, exactly.  An infinity or NaN is
+// all in its first part.
+__device__ __forceinline__ uint32_t take_part(float& f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, f);
+  uint32_t h = u & 0xffff0000u;
+  if ((u & 0x7f800000u) == 0x7f800000u) {
+    if (u & 0x007fffffu) h |= 0x00400000u;
+    f = 0.0f;
+  } else {
+    f -= __builtin_bit_cast(float, h);
+  }
+  return h >> 16;
+}
+
+template <int BK, int BN, int WM, int WN, int DY>
+struct BlockGrad {
+  static constexpr int NP = DY == DY_BF16 ? 1 : DY == DY_F16 ? 2 : 3;
+  static constexpr int NW = WM * WN, NT = 64 * NW;
+  static constexpr int TM = BK / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+  // rows per stage: two buffers of x and all parts of dY fit in LDS
+  static constexpr int D = DY == DY_BF16 ? 64 : 32;
+  static constexpr int XB = BK * 2, YB = BN * 2;  // bytes of an LDS row
+  static constexpr int X_BYTES = D * XB, Y_BYTES = D * YB;
+  static constexpr int STAGE_BYTES = X_BYTES + NP * Y_BYTES;
+  static constexpr int XCH = BK / 16, YCH = BN / 8;  // loads per row: 16 codes, 8 gradients
+  static constexpr int XL = D * XCH / NT, YL = D * YCH / NT;  // loads per thread
+  static constexpr int KSTEPS = D / 16;
+
+  static_assert(D * XCH % NT == 0 && D * YCH % NT == 0, "whole loads");
+  static_assert(2 * STAGE_BYTES + (int)sizeof(RowGroups) <= 160 * 1024, "LDS budget");
+  static_assert(NW * Strip<TN>::BYTES <= 2 * STAGE_BYTES, "the epilogue's strips fit");
+
+  static __device__ __forceinline__ lds_t* lds() {
+    __shared__ __attribute__((aligned(16))) uint8_t buf[2 * STAGE_BYTES];
+    return (lds_t*)buf;
+  }
+  template <int RB>
+  static __device__ __forceinline__ uint32_t swz_r(uint32_t k) {
+    return (((k & 1u) * 10u) + (((k >> 1) & 1u) * 4u)) & (uint32_t)(pow2_block(RB / 16) - 1);
+  }
+
+  // What a thread holds of the next stage.
+  struct Held {
+    u32x4_t x[XL];
+    uint32_t e[XL];
+    u32x4_t y[YL][DY == DY_F32 ? 2 : 1];
+  };
+
+  struct Src {
+    const uint8_t *q, *s, *y;  // first row of the range, tile's first column
+    int64_t ldq, lds, ldy;     // bytes
+    uint32_t kcols, ncols;     // valid columns of the tile
+    uint32_t rows;             // rows of the range
+    uint32_t yvec;
+  };
+
+  __device__ static __forceinline__ void load(Held& h, const Src& c, uint32_t r0) {
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      const uint32_t id = i * NT + threadIdx.x, r = id / XCH, ch = id % XCH;
+      const bool ok = r0 + r < c.rows && ch * 16 < c.kcols;
+      h.x[i] = u32x4_t{0u, 0u, 0u, 0u};
+      h.e[i] = 0u;
+      if (ok) {
+        h.x[i] = *(const u32x4_t*)(c.q + (int64_t)(r0 + r) * c.ldq + ch * 16);
+        h.e[i] = c.s[(int64_t)(r0 + r) * c.lds + ch / 8];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < YL; ++i) {
+      const uint32_t id = i * NT + threadIdx.x, r = id / YCH, n = (id % YCH) * 8;
+      constexpr int ES = DY == DY_F32 ? 4 : 2, W = DY == DY_F32 ? 2 : 1;
+      const bool ok = r0 + r < c.rows && n < c.ncols;
+#pragma unroll
+      for (int w = 0; w < W; ++w) h.y[i][w] = u32x4_t{0u, 0u, 0u, 0u};
+      if (ok) {
+        const uint8_t* p = c.y + (int64_t)(r0 + r) * c.ldy + n * ES;
+        if (c.yvec) {
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            // the last 16 bytes of a short row may start past its end
+            if (n + w * 4 < c.ncols) h.y[i][w] = ((const u32x4_t*)p)[w];
+          }
+        } else {
+          // rows that start anywhere: element by element
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (n + e >= c.ncols) break;
+            if constexpr (ES == 4)
+              h.y[i][e / 4][e % 4] = ((const uint32_t*)p)[e];
+            else
+              h.y[i][0][e / 2] |= (uint32_t)((const uint16_t*)p)[e] << (16 * (e & 1));
+          }
+        }
+      }
+    }
+  }
+
+  __device__ static __forceinline__ void store(const Held& h, lds_t* base) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      const uint32_t id = i * NT + threadIdx.x, r = id / XCH, ch = id % XCH;
+      const float s = __builtin_bit_cast(float, h.e[i] << 23);  // the exponent field is what counts
+      uint32_t o[8];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const b2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(h.x[i][d], s, false);
+        const b2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(h.x[i][d], s, true);
+        o[2 * d] = __builtin_bit_cast(uint32_t, lo);
+        o[2 * d + 1] = __builtin_bit_cast(uint32_t, hi);
+      }
+      lds_t* row = base + r * XB;
+      const uint32_t z = swz_r<XB>(r);
+      *(lds_u32x4_t*)(row + (((2 * ch) ^ z) << 4)) = u32x4_t{o[0], o[1], o[2], o[3]};
+      *(lds_u32x4_t*)(row + (((2 * ch + 1) ^ z) << 4)) = u32x4_t{o[4], o[5], o[6], o[7]};
+    }
+#pragma unroll
+    for (int i = 0; i < YL; ++i) {
+      const uint32_t id = i * NT + threadIdx.x, r = id / YCH, ch = id % YCH;
+      lds_t* at = base + X_BYTES + r * YB + ((ch ^ swz_r<YB>(r)) << 4);
+      if constexpr (DY == DY_BF16) {
+        *(lds_u32x4_t*)at = h.y[i][0];
+      } else {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t w = h.y[i][DY == DY_F32 ? e / 4 : 0][DY == DY_F32 ? e % 4 : e / 2];
+          if constexpr (DY == DY_F32)
+            f[e] = __builtin_bit_cast(float, w);
+          else
+            f[e] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> (16 * (e & 1))));
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          u32x4_t o;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const uint32_t lo = take_part(f[2 * d]);
+            o[d] = lo | take_part(f[2 * d + 1]) << 16;
+          }
+          *(lds_u32x4_t*)(at + p * Y_BYTES) = o;
+        }
+      }
+    }
+  }
+
+  // 32 columns x 16 rows as an operand: lane l holds column col0 + (l & 31),
+  // rows 16 kk + 8 (l >> 5) + 0..7.
+  template <int RB>
+  __device__ static __forceinline__ bf16x8_t frag(const lds_t* p, uint32_t col0, int kk,
+                                                  uint32_t lane) {
+    const uint32_t hi = lane >> 5, L = lane & 15u;
+    const uint32_t colb = (col0 + 16 * ((lane >> 4) & 1u) + 4 * (L & 3u)) * 2;
+    i16x4_t v[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t k = 16 * kk + 8 * hi + 4 * t + (L >> 2);
+      v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_i16x4_t*)(p + k * RB + (((colb >> 4) ^ swz_r<RB>(k)) << 4) + (colb & 8u)));
+    }
+    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+
+  __device__ static __forceinline__ void compute(f32x16_t (&acc)[FM][FN], const lds_t* base,
+                                                 uint32_t wm, uint32_t wn) {
+    const uint32_t lane = threadIdx.x & 63u;
+#pragma unroll
+    for (int kk = 0; kk < KSTEPS; ++kk) {
+      bf16x8_t x[FM], y[NP][FN];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) x[i] = frag<XB>(base, wm * TM + i * 32, kk, lane);
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          y[p][j] = frag<YB>(base + X_BYTES + p * Y_BYTES, wn * TN + j * 32, kk, lane);
+#pragma unroll
+      for (int p = NP - 1; p >= 0; --p)  // the small parts first
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y[p][j], x[i], acc[i][j], 0, 0, 0);
+    }
+  }
+
+  __device__ __attribute__((always_inline)) static void run(const BlockGradArgs& a) {
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t wm = wave / WN, wn = wave % WN;
+    const uint32_t u = logical_wg(a.remap, a.grid);
+    const uint32_t slice = a.mc.tiles.div(u);
+    const uint32_t v = u - slice * a.tiles_all;
+    const uint32_t g = a.mc.core.div(v);
+    const TileCoord t = block_coord_fast(a.mc, v - g * a.tiles);
+    // ---- rows of the group, then of this slice (whole stages)
+    uint32_t row0 = 0, rows = a.M;
+    if (a.group_m != nullptr) {
+      __shared__ RowGroups groups;
+      build_row_groups(groups, a.group_m, a.G, a.M, 1u, 1u);
+      row0 = __builtin_amdgcn_readfirstlane(groups.first_row[g]);
+      rows = __builtin_amdgcn_readfirstlane(groups.first_row[g + 1]) - row0;
+    }
+    const uint32_t stages = (rows + D - 1) / D;
+    const uint32_t per = (stages + a.split - 1) / a.split * D;
+    const uint32_t lo = slice * per < rows ? slice * per : rows;
+    const uint32_t cnt = rows - lo < per ? rows - lo : per;
+    const uint32_t k0 = t.m * BK, n0 = t.n * BN;
+    constexpr int YES = DY == DY_F32 ? 4 : 2;
+    Src c;
+    const int64_t first = (int64_t)row0 + lo;
+    c.ldq = a.ldq;
+    c.lds = a.lds;
+    c.ldy = a.lddy * YES;
+    c.q = a.Q + first * c.ldq + k0;
+    c.s = a.S + first * c.lds + k0 / kScaleBlock;
+    c.y = a.dY + first * c.ldy + (int64_t)n0 * YES;
+    c.kcols = a.K - k0 < (uint32_t)BK ? a.K - k0 : BK;
+    c.ncols = a.N - n0 < (uint32_t)BN ? a.N - n0 : BN;
+    c.rows = cnt;
+    c.yvec = a.dyvec;
+
+    f32x16_t acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+    if (cnt > 0) {
+      Held h;
+      load(h, c, 0);
+      store(h, lds());
+      uint32_t buf = 0;
+      for (uint32_t r = 0;;) {
+        r += D;
+        const bool more = r < cnt;
+        if (more) load(h, c, r);
+        __syncthreads();  // buffer buf is written, and the other one read
+        compute(acc, lds() + buf * STAGE_BYTES, wm, wn);
+        if (!more) break;
+        buf ^= 1u;
+        store(h, lds() + buf * STAGE_BYTES);
+      }
+      __syncthreads();
+    }
+    OutTile o;
+    o.rows = c.kcols;
+    o.cols = c.ncols;
+    o.add = nullptr;
+    o.ldadd_bytes = 0;
+    if (a.part != nullptr) {
+      o.kind = OUT_F32;
+      o.vec = true;
+      o.ld_bytes = (int64_t)a.pitch * 4;
+      o.dst = (uint8_t*)(a.part + (((int64_t)slice * a.G + g) * a.K + k0) * a.pitch + n0);
+    } else {
+      o.kind = a.dwkind;
+      o.vec = a.dwvec != 0;
+      const int64_t es = a.dwkind == OUT_F32 ? 4 : 2;
+      o.ld_bytes = a.lddw * es;
+      o.dst = a.dW + (g * a.stridedw + (int64_t)k0 * a.lddw + n0) * es;
+      if (a.add != nullptr) {
+        o.ldadd_bytes = a.ldadd * es;
+        o.add = a.add + (g * a.strideadd + (int64_t)k0 * a.ldadd + n0) * es;
+      }
+    }
+    store_wave_tile<FM, FN>(lds() + wave * Strip<TN>::BYTES, acc, wm * TM, wn * TN, o);
+  }
+};
+
+template <int BK, int BN, int WM, int WN, int DY>
+__global__ void __launch_bounds__(64 * WM * WN) block_grad_kernel(BlockGradArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  BlockGrad<BK, BN, WM, WN, DY>::run(a);
+#endif
+}
+
+}  // namespace bst

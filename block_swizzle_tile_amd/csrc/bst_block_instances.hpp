@@ -1,0 +1,70 @@
+// bst_block_instances.hpp -- tables of the compiled block-scaled kernels.
+// block_gemm_*.hip and block_grad.hip instantiate them; block.hip picks one
+// per call.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "bst_block_gemm.hpp"
+#include "bst_block_grad.hpp"
+
+namespace bst {
+
+struct BlockGemmInstance {
+  int bm, bn;
+  bool tb;
+  int mode;  // BlockMode
+  bool grouped;
+  int threads;
+  hipError_t (*launch)(uint32_t grid, hipStream_t, const BlockGemmArgs&);
+};
+struct BlockGemmList {
+  const BlockGemmInstance* begin;
+  int count;
+};
+BlockGemmList block_gemm_plain_t();
+BlockGemmList block_gemm_plain_n();
+BlockGemmList block_gemm_grouped_t();
+BlockGemmList block_gemm_grouped_n();
+
+struct BlockGradInstance {
+  int bk, bn, dy, depth;
+  hipError_t (*launch)(uint32_t grid, hipStream_t, const BlockGradArgs&);
+};
+struct BlockGradList {
+  const BlockGradInstance* begin;
+  int count;
+};
+BlockGradList block_grad_list();
+
+template <int BM, int BN, int WM, int WN, int ST, bool TB, int MODE, bool GR>
+hipError_t launch_block_gemm(uint32_t grid, hipStream_t st, const BlockGemmArgs& a) {
+  hipLaunchKernelGGL((block_gemm_kernel<BM, BN, WM, WN, ST, TB, MODE, GR>), dim3(grid),
+                     dim3(64 * WM * WN), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int BK, int BN, int WM, int WN, int DY>
+hipError_t launch_block_grad(uint32_t grid, hipStream_t st, const BlockGradArgs& a) {
+  hipLaunchKernelGGL((block_grad_kernel<BK, BN, WM, WN, DY>), dim3(grid), dim3(64 * WM * WN), 0,
+                     st, a);
+  return hipGetLastError();
+}
+
+#define BST_BLOCK_GEMM(BM, BN, WM, WN, ST, TB, MODE, GR)    \
+  BlockGemmInstance {                                       \
+    BM, BN, TB, MODE, GR, 64 * WM * WN,                     \
+        &launch_block_gemm<BM, BN, WM, WN, ST, TB, MODE, GR> \
+  }
+#define BST_BLOCK_GEMM_TILE(BM, BN, WM, WN, ST, TB, GR)     \
+  BST_BLOCK_GEMM(BM, BN, WM, WN, ST, TB, MODE_E8M0, GR),    \
+      BST_BLOCK_GEMM(BM, BN, WM, WN, ST, TB, MODE_F32, GR), \
+      BST_BLOCK_GEMM(BM, BN, WM, WN, ST, TB, MODE_EXACT, GR)
+#define BST_BLOCK_GEMM_TILES(TB, GR)                                                          \
+  BST_BLOCK_GEMM_TILE(32, 128, 1, 4, 4, TB, GR), BST_BLOCK_GEMM_TILE(64, 128, 1, 4, 3, TB, GR), \
+      BST_BLOCK_GEMM_TILE(128, 128, 2, 2, 3, TB, GR), BST_BLOCK_GEMM_TILE(256, 256, 2, 4, 2, TB, GR)
+
+#define BST_BLOCK_GRAD(BK, BN, WM, WN, DY) \
+  BlockGradInstance { BK, BN, DY, BlockGrad<BK, BN, WM, WN, DY>::D, &launch_block_grad<BK, BN, WM, WN, DY> }
+
+}  // namespace bst

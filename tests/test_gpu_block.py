@@ -1,0 +1,609 @@
+"""GPU tests of the block-scaled 8-bit operators (include/bst_block.h) against the definition in
+64-bit floats, computed here with torch from the codes and scales.
+
+Tolerances.  Products of two e4m3 codes are exact in fp32, and so are products of an e4m3 value and
+a bf16 part of dY.  A sum of n terms in fp32, in any order and with rounding or truncation at each
+step, is off by at most n 2^-23 sum|terms|; scaling adds the product of the two scales and one
+multiplication per block (4 more roundings).  The one rounding to the output type is off by at most
+half a step of it (2^-24, 2^-11, 2^-8 relative, or half the smallest subnormal).
+For bf16 and fp16 outputs the products run on the e4m3 instruction, which adds each 8 consecutive
+products at the largest exponent among them (the sum of the two codes' exponents, -6 for subnormal
+codes) and drops bits below 2^-13 of that power of two: the largest loses nothing, so a group loses
+less than 7 * 2^-13 * 2^(largest exponent of its 8 A codes + largest of its 8 B codes).  Codes, scales and
+restored values are exact by definition and compared bit for bit."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import block_swizzle_tile_amd as bst
+from block_swizzle_tile_amd import block as blk
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+U = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float32: 2.0 ** -150, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}
+BF, HF, FF = torch.bfloat16, torch.float16, torch.float32
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def pow2(e):
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def wide(q, s, block_rows=1):
+    """codes x scales in 64 bits."""
+    r = torch.arange(q.shape[-2], device=q.device) // block_rows
+    c = torch.arange(q.shape[-1], device=q.device) // 128
+    f = s.double() if s.dtype == FF else pow2(s.view(torch.uint8).long() - 127)
+    return q.double() * f[..., r[:, None], c[None, :]]
+
+
+def pitched(rows, cols, pitch, g, lead=()):
+    """Random finite codes; the bytes behind each row's end are NaN codes."""
+    b = torch.randint(0, 256, (*lead, rows, pitch), generator=g, device="cuda", dtype=torch.uint8)
+    b = torch.where((b & 0x7f) == 0x7f, b & 0xfe, b)
+    b[..., cols:] = 0x7f
+    return b.view(torch.float8_e4m3fn)[..., :cols]
+
+
+def scales(shape, kind, g):
+    if kind == "e8m0":
+        return torch.randint(117, 125, shape, generator=g, device="cuda", dtype=torch.uint8)
+    return torch.exp(torch.randn(shape, generator=g, device="cuda") - 6)
+
+
+def up16(n):
+    return -(-n // 16) * 16
+
+
+def operands(M, N, K, tb, kinds, g, G=0, extra=16):
+    ka, kb = kinds
+    kb_, nb = -(-K // 128), -(-N // 128)
+    A = pitched(M, K, up16(K) + extra, g)
+    lead = (G,) if G else ()
+    rows, cols = (N, K) if tb else (K, N)
+    B = pitched(rows, cols, up16(cols) + extra, g, lead)
+    return A, scales((M, kb_), ka, g), B, scales((*lead, nb, kb_) if tb else (*lead, kb_, nb), kb, g)
+
+
+def check_sum(got, ref, den, n, dtype, what="", cut=0.0):
+    assert got.dtype == dtype and got.shape == ref.shape
+    short = 0.0 if dtype == FF else cut
+    tol = ((U[dtype] * ref.abs() + short) * (1 + 2.0 ** -7) + (n + 4) * 2.0 ** -23 * den
+           + TINY[dtype])
+    err = (got.double() - ref).abs()
+    bad = ~(err <= tol)
+    assert not bool(bad.any()), "%s: %d of %d outside, first at %s: got %r, want %r" % (
+        what, int(bad.sum()), bad.numel(), bad.nonzero()[0].tolist(),
+        float(got[tuple(bad.nonzero()[0])]), float(ref[tuple(bad.nonzero()[0])]))
+
+
+def powers(q, s, block_rows, k_first):
+    """Per group of 8 K: 2^(largest exponent of its codes) times the block's scale, as [K/8][...]
+    (k_first: K is the row)."""
+    v = q.double()
+    e = pow2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6) * (1 + 2.0 ** -20))))
+    one = wide(torch.ones_like(v), s, block_rows) * torch.where(v == 0, 0.0, e)
+    one = one if k_first else one.t()
+    pad = torch.nn.functional.pad(one, (0, 0, 0, -one.shape[0] % 8))
+    return pad.view(-1, 8, pad.shape[1]).amax(1)
+
+
+def cut_product(A, sa, B, sb, tb):
+    """What the e4m3 instruction may drop of each sum (see above)."""
+    return 7 * 2.0 ** -13 * (powers(A, sa, 1, False).t() @ powers(B, sb, 128, not tb))
+
+
+def ref_product(A, sa, B, sb, tb):
+    a, b = wide(A, sa), wide(B, sb, 128)
+    b = b.transpose(-1, -2) if tb else b
+    return a @ b, a.abs() @ b.abs()
+
+
+# ------------------------------------------------------------- quantise ---
+def ref_quant(x, block_rows):
+    """Codes' values and scale bytes by the definition, in 64 bits."""
+    rows, cols = x.shape
+    rb, cb = -(-rows // block_rows), -(-cols // 128)
+    v = x.double()
+    p = torch.zeros(rb * block_rows, cb * 128, dtype=torch.float64, device=x.device)
+    p[:rows, :cols] = torch.where(v.isfinite(), v.abs(), 0.0)
+    top = p.view(rb, block_rows, cb, 128).amax(3).amax(1)
+    e = torch.full_like(top, -127.0)
+    for k in range(-127, 121):     # the smallest e with top <= 448 2^e
+        e = torch.where(top > 448 * 2.0 ** k, float(k + 1), e)
+    r = torch.arange(rows, device=x.device) // block_rows
+    c = torch.arange(cols, device=x.device) // 128
+    w = v / pow2(e)[r[:, None], c[None, :]]
+    a = w.abs()
+    step = torch.full_like(a, 2.0 ** -9)
+    for k in range(-5, 9):
+        step = torch.where(a >= 2.0 ** k, 2.0 ** (k - 3), step)
+    q = torch.sign(w) * torch.round(a / step) * step
+    return torch.where(v.isfinite(), q, math.nan), (e + 127).to(torch.uint8)
+
+
+def same_values(got, want):
+    g, w = got.double(), want.double()
+    return torch.equal(g.isnan(), w.isnan()) and torch.equal(g[~g.isnan()], w[~w.isnan()])
+
+
+QUANT_SIZES = [(1, 1), (1, 128), (3, 127), (5, 129), (2, 136), (130, 200), (257, 384), (64, 1000),
+               (1, 4096), (1000, 40)]
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+def test_quant_and_restore(dtype, block_rows):
+    for rows, cols in QUANT_SIZES:
+        say("quant", dtype, block_rows, rows, cols)
+        g = gen(rows * 7 + cols)
+        x = (torch.randn(rows, cols, generator=g, device="cuda")
+             * torch.exp(2 * torch.randn(cols, generator=g, device="cuda"))).to(dtype)
+        q, s = bst.quant_block(x, block_rows=block_rows)
+        wq, ws = ref_quant(x, block_rows)
+        assert torch.equal(s, ws) and same_values(q, wq)
+        for out in (BF, HF, FF):
+            y = bst.dequant_block(q, s, out_dtype=out, block_rows=block_rows)
+            want = wide(q, s, block_rows).clamp(-torch.finfo(out).max, torch.finfo(out).max)
+            assert same_values(y, want.to(out)), out
+
+
+def test_quant_special_values():
+    """Zeros, infinities, NaN, subnormals, the largest values, and magnitudes at and next to the
+    border 448 2^k between two scales."""
+    x = torch.zeros(10, 256, device="cuda")
+    x[1, 3], x[1, 200] = math.inf, -math.inf
+    x[2, :] = math.nan
+    x[3, 5], x[3, 6] = 1e-42, -3e-45          # subnormal: the least scale, 2^-127
+    x[4, 0], x[4, 1] = torch.finfo(FF).max, -1.0
+    x[5, 0], x[5, 128] = 448.0, math.nextafter(448.0, 1e9) * (1 + 2.0 ** -23)
+    x[6, :] = torch.linspace(-1, 1, 256)
+    x[6, 9] = math.nan
+    x[7, 0], x[7, 1] = 1.75 * 2.0 ** -100, 2.0 ** -110
+    x[8, :128] = 2.0 ** -9 * torch.arange(128)   # ties and subnormal codes
+    x[8, 127] = 448.0
+    x[9, 0], x[9, 1] = -448.0 * 2.0 ** -127, 2.0 ** -136
+    for block_rows in (1, 128):
+        q, s = bst.quant_block(x, block_rows=block_rows)
+        wq, ws = ref_quant(x, block_rows)
+        assert torch.equal(s, ws) and same_values(q, wq)
+    b = x.to(BF)
+    q, s = bst.quant_block(b)
+    wq, ws = ref_quant(b, 1)
+    assert torch.equal(s, ws) and same_values(q, wq)
+
+
+def test_restore_special_values():
+    """All codes times all E8M0 bytes, and 32-bit scales: finite stays finite (clamped to the
+    type's largest), NaN codes and scales give NaN."""
+    codes = torch.arange(256, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)
+    q = codes.repeat(256, 1).contiguous()
+    s = torch.arange(256, device="cuda", dtype=torch.uint8)[:, None].repeat(1, 2).contiguous()
+    f = pow2(s.long() - 127)
+    f = torch.where(s == 255, math.nan, f)
+    v = q.double() * f.repeat_interleave(128, 1)
+    for out in (BF, HF, FF):
+        m = torch.finfo(out).max
+        want = torch.where(v.isnan(), v, v.clamp(-m, m)).to(out)
+        assert same_values(bst.dequant_block(q, s, out_dtype=out), want)
+    # 32-bit scales: one multiplication in fp32, then the rounding
+    s32 = torch.randn(256, 2, device="cuda", generator=gen(1)) * 1e3
+    s32[0], s32[1] = math.inf, math.nan
+    y = bst.dequant_block(q[:, :256], s32, out_dtype=FF)
+    want = q.float() * s32.repeat_interleave(128, 1)
+    assert same_values(y, want)
+    x = torch.tensor([[65504.0]], device="cuda", dtype=HF)     # rounds up to 65536 in 8 bits
+    assert float(bst.dequant_block(*bst.quant_block(x), out_dtype=HF)) == 65504.0
+
+
+def test_quant_layouts():
+    """Column slices (any pitch and base), given outputs, and nothing written outside them."""
+    big = torch.randn(50, 301, device="cuda", generator=gen(3)).to(BF)
+    x = big[3:45, 7:207]                      # 2-byte aligned rows of 200
+    Q = torch.full((42, 233), 0x55, dtype=torch.uint8, device="cuda")
+    S = torch.full((42, 5), 0x55, dtype=torch.uint8, device="cuda")
+    q, s = bst.quant_block(x, Q.view(torch.float8_e4m3fn)[:, 5:205], S[:, 1:3])
+    wq, ws = ref_quant(x, 1)
+    assert torch.equal(S[:, 1:3], ws) and same_values(q, wq)
+    assert bool((Q[:, :5] == 0x55).all()) and bool((Q[:, 205:] == 0x55).all())
+    assert bool((S[:, 0] == 0x55).all()) and bool((S[:, 3:] == 0x55).all())
+    X = torch.full((42, 333), 9.0, dtype=HF, device="cuda")
+    bst.dequant_block(q, s, X[:, 3:203])
+    assert same_values(X[:, 3:203], wide(q, s).to(HF))
+    assert bool((X[:, :3] == 9).all()) and bool((X[:, 203:] == 9).all())
+    for shape in ((0, 64), (5, 0)):
+        q, s = bst.quant_block(torch.zeros(shape, device="cuda"))
+        assert q.shape == shape and bst.dequant_block(q, s).shape == shape
+
+
+def test_offsets_past_32_bits():
+    """Rows whose byte offsets pass 2^32: a pitch of 8 MiB - 16 codes over 600 rows (5 GB)."""
+    rows, pitch = 600, (8 << 20) - 16 - 256
+    buf = torch.empty(rows * pitch, dtype=torch.uint8, device="cuda")
+    A = buf.view(rows, pitch).view(torch.float8_e4m3fn)[:, :136]
+    A.view(torch.uint8).copy_(pitched(rows, 136, 144, gen(1)).view(torch.uint8))
+    buf.view(rows, pitch)[:, 136:144] = 0x7f
+    g = gen(2)
+    sa = scales((rows, 2), "e8m0", g)
+    B = pitched(136, 48, 48, g)
+    sb = scales((2, 1), "e8m0", g)
+    ref, den = ref_product(A, sa, B, sb, False)
+    for tile in ((32, 128), (128, 128), (256, 256)):
+        C = bst.gemm_block_scaled(A, B, sa, sb, out_dtype=FF,
+                                  sched=bst.make_sched(tile=tile, offset=2, split_k=1))
+        check_sum(C, ref, den, 136, FF, str(tile))
+    dY = torch.randn(rows, 40, device="cuda", generator=g).to(BF)
+    x = wide(A, sa)
+    check_sum(bst.weight_grad(A, sa, dY), x.t() @ dY.double(), x.abs().t() @ dY.double().abs(), rows, FF)
+    assert same_values(bst.dequant_block(A, sa), wide(A, sa).to(BF))
+    q, s = bst.quant_block(wide(A, sa).to(BF))
+    assert torch.equal(wide(q, s), wide(A, sa))
+
+
+# -------------------------------------------------------------- products ---
+TILES = [(32, 128), (64, 128), (128, 128), (256, 256)]
+KINDS = [("e8m0", "e8m0"), ("f32", "f32"), ("e8m0", "f32"), ("f32", "e8m0")]
+SIZES = [(1, 1, 1), (1, 16, 128), (5, 130, 200), (33, 257, 129), (64, 300, 1000), (129, 136, 256),
+         (300, 520, 640), (1, 1000, 2055), (257, 129, 383)]
+
+
+@pytest.mark.parametrize("tb", [False, True])
+@pytest.mark.parametrize("kinds", KINDS)
+def test_product(kinds, tb):
+    for M, N, K in SIZES:
+        A, sa, B, sb = operands(M, N, K, tb, kinds, gen(M + N + K))
+        ref, den = ref_product(A, sa, B, sb, tb)
+        cut = cut_product(A, sa, B, sb, tb)
+        for tile, split, out in [((0, 0), 0, BF), ((0, 0), 0, FF), ((32, 128), 1, FF),
+                                 ((64, 128), 3, HF), ((128, 128), 1, FF), ((128, 128), 2, BF),
+                                 ((256, 256), 1, BF), ((256, 256), 5, FF),
+                                 ((32, 128), 2, HF), ((256, 256), 2, HF)]:
+            say("product", kinds, tb, M, N, K, tile, split, out)
+            C = torch.full((M, N + 3), 7.0, dtype=out, device="cuda")
+            bst.gemm_block_scaled(A, B, sa, sb, C[:, :N], trans_b=tb,
+                                  sched=bst.make_sched(tile=tile, offset=3, split_k=split,
+                                                       xcd_remap=1))
+            check_sum(C[:, :N], ref, den, K, out, str((tile, split)), cut)
+            assert bool((C[:, N:] == 7).all())
+
+
+@pytest.mark.parametrize("M", [1, 2, 16, 31, 32, 48, 64, 65, 200])
+def test_product_default_schedule(M):
+    """Few rows (single tokens) over longer K, where the split is chosen by the sizes."""
+    for tb in (False, True):
+        for N, K in [(512, 4096), (1040, 1552), (4096, 512)]:
+            A, sa, B, sb = operands(M, N, K, tb, ("e8m0", "f32"), gen(M), extra=0)
+            ref, den = ref_product(A, sa, B, sb, tb)
+            say("default", M, N, K, tb)
+            cut = cut_product(A, sa, B, sb, tb)
+            check_sum(bst.gemm_block_scaled(A, B, sa, sb, trans_b=tb), ref, den, K, BF, "", cut)
+            C = bst.gemm_block_scaled(A, B, sa, sb, trans_b=tb, out_dtype=FF)
+            check_sum(C, ref, den, K, FF)
+            C2 = bst.gemm_block_scaled(A, B, sa.view(torch.float8_e8m0fnu), sb, trans_b=tb,
+                                       out_dtype=FF)
+            assert torch.equal(C, C2)      # the same bits, call after call
+
+
+def test_product_large_tiles_match_swizzles():
+    """Every window order gives the same bits; the default picks the large tile here."""
+    M, N, K = 2048, 2304, 384
+    A, sa, B, sb = operands(M, N, K, True, ("f32", "f32"), gen(5))
+    ref, den = ref_product(A, sa, B, sb, True)
+    cut = cut_product(A, sa, B, sb, True)
+    C0 = bst.gemm_block_scaled(A, B, sa, sb, trans_b=True)
+    check_sum(C0, ref, den, K, BF, "", cut)
+    for d in ("zn", "nz", "raster"):
+        for off, remap in ((1, 0), (3, 1), (100, 1)):
+            C = bst.gemm_block_scaled(A, B, sa, sb, trans_b=True, sched=bst.make_sched(
+                tile=(256, 256), offset=off, direction=d, xcd_remap=remap))
+            assert torch.equal(C, C0)
+
+
+def test_product_nan_and_zero():
+    """A NaN code stays in its row (or column); K = 0 and empty outputs; NaN scale bytes."""
+    for tile in TILES:
+        for kinds in KINDS[:2]:
+            A, sa, B, sb = operands(70, 140, 300, True, kinds, gen(9))
+            ref, den = ref_product(A, sa, B, sb, True)
+            A = A.clone()
+            A.view(torch.uint8)[5, 299] = 0x7f
+            B = B.clone()
+            B.view(torch.uint8)[130, 0] = 0xff
+            A = torch.nn.functional.pad(A.view(torch.uint8), (0, 4), value=0x7f).view(A.dtype)[:, :300]
+            B = torch.nn.functional.pad(B.view(torch.uint8), (0, 4), value=0x7f).view(B.dtype)[:, :300]
+            C = bst.gemm_block_scaled(A, B, sa, sb, trans_b=True, out_dtype=FF,
+                                      sched=bst.make_sched(tile=tile))
+            nan = torch.zeros_like(C, dtype=torch.bool)
+            nan[5], nan[:, 130] = True, True
+            assert torch.equal(C.isnan(), nan)
+            keep = ~nan
+            check_sum(C[keep], ref[keep], den[keep], 300, FF)
+    e = torch.empty
+    z = bst.gemm_block_scaled(e(3, 0, device="cuda").to(torch.float8_e4m3fn),
+                              e(0, 5, device="cuda").to(torch.float8_e4m3fn),
+                              e(3, 0, device="cuda", dtype=torch.uint8),
+                              e(0, 1, device="cuda", dtype=torch.uint8))
+    assert z.shape == (3, 5) and bool((z == 0).all())
+    A, sa, B, sb = operands(4, 16, 128, False, KINDS[0], gen(9))
+    assert bst.gemm_block_scaled(A[:0], B, sa[:0], sb).shape == (0, 16)
+    sa[2] = 255
+    C = bst.gemm_block_scaled(A, B, sa, sb)
+    assert bool(C[2].isnan().all()) and not bool(C[[0, 1, 3]].isnan().any())
+
+
+# ------------------------------------------------------ grouped products ---
+GROUPS = [([5], 5), ([0, 0, 0], 7), ([1, 0, 3, 0], 9), ([33, -4, 1, 64], 98), ([300, 1, 0, 200], 501),
+          ([10, 500, 3], 100), ([1] * 64, 64), ([2] * 1000 + [0] * 24, 2000)]
+
+
+def spans(sizes, total):
+    at, out = 0, []
+    for n in sizes:
+        n = min(max(n, 0), total - at)
+        out.append((at, at + n))
+        at += n
+    return out
+
+
+@pytest.mark.parametrize("tb", [False, True])
+@pytest.mark.parametrize("kinds", KINDS[:3])
+def test_grouped_product(kinds, tb):
+    for sizes, total in GROUPS:
+        G = len(sizes)
+        N, K = (24, 40) if G > 100 else (200, 264)
+        A, sa, B, sb = operands(total, N, K, tb, kinds, gen(G + total), G=G)
+        gm = torch.tensor(sizes, dtype=torch.int32, device="cuda")
+        for tile, out in [((0, 0), FF), ((0, 0), BF)] + [(t, o) for t in (TILES if G < 100 else TILES[:1])
+                                                         for o in (FF, HF)]:
+            say("grouped", kinds, tb, G, total, tile, out)
+            C = torch.full((total, N), 7.0, dtype=out, device="cuda")
+            bst.grouped_gemm_block_scaled(A, B, gm, sa, sb, C, trans_b=tb,
+                                          sched=bst.make_sched(tile=tile, offset=2, xcd_remap=1))
+            for g, (lo, hi) in enumerate(spans(sizes, total)):
+                if hi > lo:
+                    ref, den = ref_product(A[lo:hi], sa[lo:hi], B[g], sb[g], tb)
+                    cut = cut_product(A[lo:hi], sa[lo:hi], B[g], sb[g], tb) if out != FF else 0.0
+                    check_sum(C[lo:hi], ref, den, K, out, "group %d" % g, cut)
+            assert bool((C[spans(sizes, total)[-1][1]:] == 7).all())
+
+
+# -------------------------------------------------------------- gradients ---
+def kept(M, K, g):
+    return pitched(M, K, up16(K) + 16, g), scales((M, -(-K // 128)), "e8m0", g)
+
+
+def grads(M, N, dtype, g, aligned):
+    pad = -(-N // 8) * 8 if aligned else N | 1
+    return (torch.randn(M, pad, generator=g, device="cuda") * 0.1).to(dtype)[:, :N]
+
+
+GRAD_SIZES = [(1, 1, 1), (3, 17, 5), (64, 128, 128), (65, 130, 250), (200, 256, 136), (31, 300, 24),
+              (1000, 264, 391)]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_weight_grad(dtype, aligned):
+    for M, K, N in GRAD_SIZES:
+        g = gen(M + K + N)
+        q, s = kept(M, K, g)
+        dY = grads(M, N, dtype, g, aligned)
+        x = wide(q, s)
+        ref, den = x.t() @ dY.double(), x.abs().t() @ dY.double().abs()
+        n = M * {BF: 1, HF: 2, FF: 3}[dtype]
+        for tile, split, out in [((0, 0), 0, FF), ((128, 128), 1, BF), ((128, 128), 3, HF),
+                                 ((256, 256), 1, FF), ((256, 256), 4, FF)]:
+            say("grad", dtype, aligned, M, K, N, tile, split, out)
+            sched = bst.make_sched(tile=tile, offset=2, split_k=split)
+            check_sum(bst.weight_grad(q, s, dY, out_dtype=out, sched=sched), ref, den, n, out,
+                      str((tile, split)))
+            add = torch.randn(K, N, generator=g, device="cuda").to(out)
+            want, d2 = ref + add.double(), den + add.double().abs()
+            check_sum(bst.weight_grad(q, s, dY, add=add, sched=sched), want, d2, n + 1, out)
+            acc = torch.full((K, N + 5), 3.0, dtype=out, device="cuda")    # in place, pitched
+            acc[:, :N] = add
+            bst.weight_grad(q, s, dY, acc[:, :N], add=acc[:, :N], sched=sched)
+            check_sum(acc[:, :N], want, d2, n + 1, out)
+            assert bool((acc[:, N:] == 3).all())
+
+
+def test_weight_grad_empty_and_special():
+    g = gen(4)
+    q, s = kept(0, 40, g)
+    dY = torch.zeros(0, 24, dtype=BF, device="cuda")
+    add = torch.randn(40, 24, device="cuda", generator=g)
+    assert bool((bst.weight_grad(q, s, dY) == 0).all())
+    assert torch.equal(bst.weight_grad(q, s, dY, add=add), add)
+    # infinities and NaN of dY stay in their column, whatever the type and the parts it is cut into
+    for dtype in (BF, HF, FF):
+        q, s = kept(100, 64, g)
+        q.view(torch.uint8)[:, 0] = 0x38      # ones: no zero times infinity in row 0
+        dY = torch.randn(100, 48, device="cuda", generator=g).to(dtype)
+        dY[7, 3], dY[9, 5] = math.inf, math.nan
+        dW = bst.weight_grad(q, s, dY)
+        assert float(dW[0, 3]) == math.inf and bool(dW[:, 5].isnan().all())
+        rest = [c for c in range(48) if c not in (3, 5)]
+        assert bool(dW[:, rest].isfinite().all())
+    # the whole range of fp32: parts that add up to the value exactly
+    q = torch.ones(32, 16, device="cuda").to(torch.float8_e4m3fn)
+    s = torch.full((32, 1), 127, dtype=torch.uint8, device="cuda")
+    v = torch.tensor([torch.finfo(FF).max, 1 + 2.0 ** -23, 1e-30 * (1 + 2.0 ** -20), -2.0 ** 100 / 3],
+                     device="cuda")
+    dY = torch.zeros(32, 4, device="cuda")
+    dY[13] = v
+    assert torch.equal(bst.weight_grad(q, s, dY), v.expand(16, 4))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_grouped_weight_grad(dtype):
+    for sizes, total in GROUPS:
+        G = len(sizes)
+        K, N = (24, 40) if G > 100 else (136, 200)
+        g = gen(G)
+        q, s = kept(total, K, g)
+        dY = grads(total, N, dtype, g, True)
+        gm = torch.tensor(sizes, dtype=torch.int32, device="cuda")
+        x = wide(q, s)
+        add = torch.randn(G, K, N, generator=g, device="cuda")
+        for tile, split in [((0, 0), 0), ((128, 128), 1), ((256, 256), 3)]:
+            say("grouped grad", dtype, G, total, tile, split)
+            sched = bst.make_sched(tile=tile, offset=2, split_k=split)
+            dW = bst.grouped_weight_grad(q, s, dY, gm, sched=sched)
+            dA = bst.grouped_weight_grad(q, s, dY, gm, add=add, sched=sched)
+            for k, (lo, hi) in enumerate(spans(sizes, total)):
+                if G > 100 and k % 97:
+                    continue
+                a, b = x[lo:hi], dY[lo:hi].double()
+                ref, den = a.t() @ b, a.abs().t() @ b.abs()
+                check_sum(dW[k], ref, den, 2 * (hi - lo), FF)
+                check_sum(dA[k], ref + add[k].double(), den + add[k].double().abs(),
+                          2 * (hi - lo) + 1, FF)
+                if hi == lo:
+                    assert torch.equal(dA[k], add[k]) and bool((dW[k] == 0).all())
+
+
+# ------------------------------------------------ together, as they are used ---
+def test_linear_layer_forward_backward_and_differences():
+    """A linear layer's step: the 8-bit forward product, the gradient of the input from the same
+    weight codes, and the gradient of the weight from the kept codes, each against its formula and
+    against central differences of the scalar f = sum(dy * (x w)) in 64 bits (f is linear in x and
+    in w, so a difference of step 1 has no error beyond 64-bit rounding)."""
+    M, K, N = 150, 264, 136
+    g = gen(11)
+    x = torch.randn(M, K, generator=g, device="cuda").to(BF)
+    w = (torch.randn(K, N, generator=g, device="cuda") / K ** 0.5).to(BF)
+    dy = torch.randn(M, N, generator=g, device="cuda").to(BF)
+    xq, xs = bst.quant_block(x)
+    wq, ws = bst.quant_block(w, block_rows=128)
+    y = bst.gemm_block_scaled(xq, wq, xs, ws, out_dtype=FF)
+    dyq, dys = bst.quant_block(dy)
+    dx = bst.gemm_block_scaled(dyq, wq, dys, ws, trans_b=True, out_dtype=FF)
+    dw = bst.weight_grad(xq, xs, dy)
+    X, W, D, DQ = wide(xq, xs), wide(wq, ws, 128), dy.double(), wide(dyq, dys)
+    check_sum(y, X @ W, X.abs() @ W.abs(), K, FF)
+    check_sum(dx, DQ @ W.t(), DQ.abs() @ W.abs().t(), N, FF)
+    check_sum(dw, X.t() @ D, X.abs().t() @ D.abs(), M, FF)
+
+    def f(x_, w_, d_):
+        return float((d_ * (x_ @ w_)).sum())
+    for i, j in [(0, 0), (149, 135), (77, 128)]:
+        for t, out, d_, other in ((X, dx, DQ, "x"), (W, dw, D, "w")):
+            r, c = min(i, t.shape[0] - 1), min(j, t.shape[1] - 1)
+            hi, lo = t.clone(), t.clone()
+            hi[r, c] += 1
+            lo[r, c] -= 1
+            diff = (f(hi, W, d_) - f(lo, W, d_)) / 2 if other == "x" else (f(X, hi, d_) - f(X, lo, d_)) / 2
+            den = float((d_.abs() @ W.abs().t())[r, c] if other == "x" else (X.abs().t() @ d_.abs())[r, c])
+            assert abs(diff - float(out[r, c])) <= (max(M, N) + 4) * 2.0 ** -23 * den + 1e-9
+    # the codes restored, as another operator of the backward pass would read them
+    assert same_values(bst.dequant_block(xq, xs), X.to(BF))
+
+
+def test_experts_step():
+    """A mixture's layer: grouped product, gradient of its input, gradient of every expert."""
+    sizes, total, K, N = [40, 0, 129, 31], 210, 256, 144
+    G = len(sizes)
+    g = gen(12)
+    x = torch.randn(total, K, generator=g, device="cuda").to(BF)
+    w = torch.randn(G, K, N, generator=g, device="cuda") / 16
+    gm = torch.tensor(sizes, dtype=torch.int32, device="cuda")
+    xq, xs = bst.quant_block(x)
+    pairs = [bst.quant_block(w[e], block_rows=128) for e in range(G)]
+    wq = torch.stack([p[0].view(torch.uint8) for p in pairs]).view(torch.float8_e4m3fn)
+    ws = torch.stack([p[1] for p in pairs])
+    dy = torch.randn(total, N, generator=g, device="cuda").to(BF)
+    dyq, dys = bst.quant_block(dy)
+    y = bst.grouped_gemm_block_scaled(xq, wq, gm, xs, ws, out_dtype=FF)
+    dx = bst.grouped_gemm_block_scaled(dyq, wq, gm, dys, ws, trans_b=True, out_dtype=FF)
+    dw = bst.grouped_weight_grad(xq, xs, dy, gm)
+    X, D, DQ = wide(xq, xs), dy.double(), wide(dyq, dys)
+    for e, (lo, hi) in enumerate(spans(sizes, total)):
+        W = wide(wq[e], ws[e], 128)
+        a, d, dq = X[lo:hi], D[lo:hi], DQ[lo:hi]
+        check_sum(y[lo:hi], a @ W, a.abs() @ W.abs(), K, FF)
+        check_sum(dx[lo:hi], dq @ W.t(), dq.abs() @ W.abs().t(), N, FF)
+        check_sum(dw[e], a.t() @ d, a.abs().t() @ d.abs(), hi - lo, FF)
+
+
+def test_streams_and_graphs():
+    """Calls on two streams at once, each with a split (a workspace each), then a captured step
+    replayed with new inputs between eager calls: every result has the eager call's bits."""
+    M, N, K = 24, 256, 2048
+    sets = [operands(M, N, K, tb, ("e8m0", "f32"), gen(20 + tb)) for tb in (False, True)]
+    want = [bst.gemm_block_scaled(A, B, sa, sb, trans_b=bool(i)) for i, (A, sa, B, sb) in enumerate(sets)]
+    assert bst.block_workspace_bytes(0, 1, M, N, K) > 0
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(20):
+        for i, (A, sa, B, sb) in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                got[i] = bst.gemm_block_scaled(A, B, sa, sb, trans_b=bool(i))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+    x = torch.randn(M, K, device="cuda").to(BF)
+    _, _, B, sb = sets[0]
+    dy = torch.randn(M, N, device="cuda").to(BF)
+    acc = torch.zeros(K, N, device="cuda")
+
+    def step():
+        q, s = bst.quant_block(x)
+        y = bst.gemm_block_scaled(q, B, s, sb)
+        bst.weight_grad(q, s, dy, acc, add=acc)
+        return y
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for _ in range(2):          # two graphs of the same step
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            y = step()
+        graphs.append((gr, y))
+    for r in range(4):
+        x.copy_(torch.randn(M, K, device="cuda", generator=gen(r)).to(BF))
+        acc.zero_()
+        ref = step()
+        once = acc.clone()
+        for gr, y in graphs:
+            acc.zero_()
+            gr.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, ref) and torch.equal(acc, once), r
+
+
+def test_noncurrent_stream_pointer_and_refusals():
+    A, sa, B, sb = operands(40, 64, 256, False, KINDS[0], gen(1))
+    with pytest.raises(ValueError):
+        bst.gemm_block_scaled(A, B, sa[:, :1], sb)
+    with pytest.raises(TypeError):
+        bst.gemm_block_scaled(A.view(torch.uint8), B, sa, sb)
+    with pytest.raises(TypeError):
+        bst.gemm_block_scaled(A, B, sa.to(torch.int32), sb)
+    with pytest.raises(ValueError):
+        bst.gemm_block_scaled(A.cpu(), B, sa, sb)
+    with pytest.raises(ValueError):
+        bst.quant_block(torch.zeros(4, 8, device="cuda").t())
+    with pytest.raises(bst.BstError):
+        odd = torch.zeros(4, 33, device="cuda").to(torch.float8_e4m3fn)     # rows of 33 bytes
+        bst.gemm_block_scaled(odd, torch.zeros(33, 16, device="cuda").to(torch.float8_e4m3fn),
+                              torch.zeros(4, 1, dtype=torch.uint8, device="cuda"),
+                              torch.zeros(1, 1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(TypeError):
+        bst.weight_grad(A, torch.ones(40, 2, device="cuda"), torch.zeros(40, 8, device="cuda"))
+    with pytest.raises(ValueError):
+        bst.weight_grad(A, sa, torch.ones(1, 1, device="cuda").expand(40, 8))   # a broadcast dY
+    with pytest.raises(bst.BstError):
+        bst.gemm_block_scaled(A, B, sa, sb, sched=bst.make_sched(split_k=2),
+                              workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert blk.E8M0 == 8 and ctypes.sizeof(ctypes.c_void_p) == 8
