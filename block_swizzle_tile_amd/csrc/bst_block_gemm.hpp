@@ -86,38 +86,78 @@ struct BlockGemm {
     __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
   }
 
+  // A lane's part of the DMA addressing.  Instruction x of a wave covers 8
+  // rows of A (or of a transposed B), or RPB K rows of B; the lane's offset
+  // is its offset in the wave's first rows with the chunk index exchanged by
+  // an XOR that only depends on the instruction, and the rows go to the scalar
+  // offset: two registers hold what a register per instruction would (those
+  // did not fit beside the accumulators of the 256 x 256 tile).
   struct Lanes {
-    uint32_t a_off[A_IPW], b_off[B_IPW];  // byte offset in the stage's panel, or kOob
-    uint32_t a_k[A_IPW], b_k[B_IPW];      // K index of the access inside the stage
+    uint32_t a_row, b_row;  // offset of the lane's row in an instruction's rows
+    uint32_t a_ch, b_ch;    // its chunk, before the instruction's XOR
+    uint32_t inside;        // bit x: access x is inside the matrix (rows; columns of B)
+    uint32_t tail;          // bit x: and inside K in the last, partial stage
     uint32_t s_off;
   };
+  static constexpr int RPB = TB ? 8 : 1024 / BN;
+  // instruction x of wave w: its XOR and its first row (or K row)
+  static __device__ __forceinline__ uint32_t a_xor(uint32_t w, int x) { return (w * A_IPW + x) & 7u; }
+  static __device__ __forceinline__ uint32_t b_xor(uint32_t w, int x) {
+    return TB ? (w * B_IPW + x) & 7u : ((w * B_IPW + x) * RPB) & 7u & BSWZ;
+  }
 
   struct Src {
     const uint8_t *a, *b, *sa;  // panels of the task at K = 0
     int64_t ldb;
-    uint32_t K, sa_f32, wave;
+    uint32_t lda32, ldb32;
+    uint32_t K, kt1, sa_f32, wave;
   };
 
-  // DMA of stage kt (K rows kt*128 ..) into buffer s.  Accesses at or past K
-  // are sent out of the descriptor's range and write zeros.
-  __device__ static __forceinline__ void issue(const Src& c, const Lanes& ln, uint32_t kt,
-                                               uint32_t s) {
-    lds_t* base = lds() + s * STAGE_BYTES;
-    const uint32_t left = c.K - kt * 128u;
-    const u32x4_t ra = make_desc(c.a + (uint64_t)kt * 128u);
-    const u32x4_t rb = make_desc(c.b + (TB ? (int64_t)kt * 128 : (int64_t)kt * 128 * c.ldb));
-#pragma unroll
-    for (int i = 0; i < A_IPW; ++i)
-      dma16(ra, base + (c.wave * A_IPW + i) * 1024, ln.a_k[i] < left ? ln.a_off[i] : kOob, 0u);
-#pragma unroll
-    for (int i = 0; i < B_IPW; ++i)
-      dma16(rb, base + A_BYTES + (c.wave * B_IPW + i) * 1024,
-            ln.b_k[i] < left ? ln.b_off[i] : kOob, 0u);
-    lds_t* sdst = base + A_BYTES + B_BYTES + (c.wave < (uint32_t)SA_N ? c.wave * 256u : SA_BYTES);
+  // Where one stage's DMA reads and writes.
+  struct Stage {
+    u32x4_t ra, rb;
+    lds_t* base;
+    uint32_t live;  // bit x: this lane's access x is inside its matrix
+    uint32_t a_ch, b_ch;
+  };
+
+  // Stage kt (K rows kt*128 ..) into buffer s.  A stage past the slice's last
+  // is issued all the same, with every access out of range: the counts in
+  // flight then never depend on where the loop is, and what it writes (zeros)
+  // is never read.
+  __device__ static __forceinline__ Stage stage(const Src& c, const Lanes& ln, uint32_t kt,
+                                                uint32_t s) {
+    Stage st;
+    st.ra = make_desc(c.a + (uint64_t)kt * 128u);
+    st.rb = make_desc(c.b + (TB ? (int64_t)kt * 128 : (int64_t)kt * 128 * c.ldb));
+    st.base = lds() + s * STAGE_BYTES;
+    st.a_ch = fresh_v(ln.a_ch);  // offsets are made anew for every stage, not kept
+    st.b_ch = fresh_v(ln.b_ch);
+    st.live = kt >= c.kt1 ? 0u : (kt + 1) * 128u <= c.K ? ln.inside : ln.tail;
+    return st;
+  }
+  static constexpr int ND = A_IPW + B_IPW;
+  template <int X>
+  __device__ static __forceinline__ void dma_one(const Src& c, const Lanes& ln, const Stage& st) {
+    if constexpr (X < A_IPW) {
+      const uint32_t off = ln.a_row + ((st.a_ch ^ a_xor(c.wave, X)) << 4);
+      dma16(st.ra, st.base + (c.wave * A_IPW + X) * 1024, (st.live >> X) & 1u ? off : kOob,
+            (c.wave * A_IPW + X) * 8 * c.lda32);
+    } else {
+      constexpr int x = X - A_IPW;
+      const uint32_t off = ln.b_row + ((st.b_ch ^ b_xor(c.wave, x)) << 4);
+      dma16(st.rb, st.base + A_BYTES + (c.wave * B_IPW + x) * 1024,
+            (st.live >> X) & 1u ? off : kOob, (c.wave * B_IPW + x) * RPB * c.ldb32);
+    }
+  }
+  __device__ static __forceinline__ void dma_scales(const Src& c, const Lanes& ln, const Stage& st,
+                                                    uint32_t kt) {
+    lds_t* dst = st.base + A_BYTES + B_BYTES + (c.wave < (uint32_t)SA_N ? c.wave * 256u : SA_BYTES);
+    const uint32_t v = kt < c.kt1 ? ln.s_off : kOob;
     if (c.sa_f32)
-      dma4(make_desc(c.sa + (uint64_t)kt * 4u), sdst, ln.s_off, 0u);
+      dma4(make_desc(c.sa + (uint64_t)kt * 4u), dst, v, 0u);
     else
-      dma1(make_desc(c.sa + kt), sdst, ln.s_off);
+      dma1(make_desc(c.sa + kt), dst, v);
   }
 
   // K % 16 != 0: the last chunk of a row holds bytes past K, which may be
@@ -139,28 +179,53 @@ struct BlockGemm {
     __syncthreads();
   }
 
-  __device__ static __forceinline__ i32x8_t rows_frag(const lds_t* base, uint32_t row, int kk,
-                                                      uint32_t hi) {
-    const lds_t* rp = base + row * 128;
-    const u32x4_t x = *(const lds_u32x4_t*)(rp + (((4 * kk + hi) ^ swz(row)) << 4));
-    const u32x4_t y = *(const lds_u32x4_t*)(rp + (((4 * kk + 2 + hi) ^ swz(row)) << 4));
+  // Operand fragments: lane l holds row (l & 31) of a 32-row fragment, K =
+  // 64 kk + 16 (l >> 5) + 0..15 and 32 more.  Rows of 128 bytes with their
+  // chunks XORed by swz(row): fragment i of a wave lies 32 i rows on, which
+  // only flips bit 2 of the XOR for odd i, so four lane addresses (two chunks,
+  // plain and flipped) serve all of them with constant offsets.
+  struct RowPtrs {
+    const lds_t* p[4];
+  };
+  __device__ static __forceinline__ RowPtrs row_ptrs(const lds_t* base, uint32_t row0) {
+    const uint32_t lane = threadIdx.x & 63u, row = row0 + (lane & 31u), hi = lane >> 5;
+    RowPtrs r;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      r.p[v] = base + row * 128 + ((((v & 1) * 2 + hi) ^ swz(row) ^ ((v >> 1) * 4u)) << 4);
+    return r;
+  }
+  __device__ static __forceinline__ i32x8_t rows_frag(const RowPtrs& r, int i, int kk) {
+    const int s = 2 * (kk ^ (i & 1));
+    const u32x4_t x = *(const lds_u32x4_t*)(r.p[s] + i * 4096);
+    const u32x4_t y = *(const lds_u32x4_t*)(r.p[s + 1] + i * 4096);
     return i32x8_t{(int)x[0], (int)x[1], (int)x[2], (int)x[3],
                    (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
   }
 
   // B fragment from K rows: four transposing reads (8 K values each) in the
-  // K order of rows_frag.
-  __device__ static __forceinline__ i32x8_t cols_frag(const lds_t* lb, uint32_t col0, int kk,
-                                                      uint32_t lane) {
-    const uint32_t hi = lane >> 5, L = lane & 15u;
-    const uint32_t colb = col0 + 16 * ((lane >> 4) & 1u) + 8 * (L & 1u);
+  // K order of rows_frag.  A lane's K rows differ by multiples of 8, which
+  // leave the XOR of the columns' chunk alone, and fragment j flips bit 1 of
+  // the chunk: one address per j.
+  struct ColPtrs {
+    const lds_t* p[FN];
+  };
+  __device__ static __forceinline__ ColPtrs col_ptrs(const lds_t* lb, uint32_t wn) {
+    const uint32_t lane = threadIdx.x & 63u, hi = lane >> 5, L = lane & 15u;
+    const uint32_t k = 16 * hi + (L >> 1);
+    const uint32_t ch = (wn * TN) / 16 + ((lane >> 4) & 1u);
+    ColPtrs r;
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      r.p[j] = lb + k * BN + (((ch ^ (2u * j)) ^ swz_b(k)) << 4) + 8 * (L & 1u);
+    return r;
+  }
+  __device__ static __forceinline__ i32x8_t cols_frag(const ColPtrs& r, int j, int kk) {
     i32x2_t v[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const uint32_t k = 64 * kk + 32 * (t >> 1) + 16 * hi + 8 * (t & 1) + (L >> 1);
+    for (int t = 0; t < 4; ++t)
       v[t] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-          (lds_i32x2_t*)(lb + k * BN + (((colb >> 4) ^ swz_b(k)) << 4) + (colb & 8u)));
-    }
+          (lds_i32x2_t*)(r.p[j] + (64 * kk + 32 * (t >> 1) + 8 * (t & 1)) * BN));
     return i32x8_t{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
   }
 
@@ -177,18 +242,36 @@ struct BlockGemm {
     return __builtin_bit_cast(bf16x8_t, o);
   }
 
-  // The products of one stage.
+  // The products of one stage, with the DMA of a later one (`next`) between
+  // them.  The order is fixed by hand, one matrix instruction per slot:
+  // behind each go its share of the DMA instructions (one per slot from the
+  // first: with two stages they have only this step to land in), the LDS
+  // reads of the operands that the slots ahead need, and with 32-bit scales
+  // half of the 16 multiply-adds of the sub-tile before, which the vector unit
+  // does while the matrix unit works on this one.
   __device__ static __forceinline__ void compute(f32x16_t (&acc)[FM][FN], const lds_t* base,
                                                  uint32_t wm, uint32_t wn, uint32_t sb_raw,
-                                                 bool sa_f32, bool sb_f32) {
-    const uint32_t lane = threadIdx.x & 63u, l32 = lane & 31u, hi = lane >> 5;
+                                                 bool sb_f32, const Src& c, const Lanes& ln,
+                                                 const Stage& next) {
+    const uint32_t l32 = threadIdx.x & 31u;
     const lds_t* lb = base + A_BYTES;
-    auto a_frag = [&](int i, int kk) { return rows_frag(base, wm * TM + i * 32 + l32, kk, hi); };
+    const RowPtrs pa = row_ptrs(base, wm * TM);
+    const auto pb = [&] {
+      if constexpr (TB) return row_ptrs(lb, wn * TN);
+      else return col_ptrs(lb, wn);
+    }();
+    auto a_frag = [&](int i, int kk) { return rows_frag(pa, i, kk); };
     auto b_frag = [&](int j, int kk) {
-      if constexpr (TB)
-        return rows_frag(lb, wn * TN + j * 32 + l32, kk, hi);
-      else
-        return cols_frag(lb, wn * TN + j * 32, kk, lane);
+      if constexpr (TB) return rows_frag(pb, j, kk);
+      else return cols_frag(pb, j, kk);
+    };
+    constexpr int NS = 2 * FM * FN;           // slots
+    constexpr int DS = NS < ND ? NS : ND;     // slots that carry DMA
+    auto slot_dma = [&](auto q) {
+      constexpr int Q = decltype(q)::value;
+      if constexpr (Q < DS)
+        static_for_range<Q * ND / DS, (Q + 1) * ND / DS>(
+            [&](auto x) { dma_one<decltype(x)::value>(c, ln, next); });
     };
     uint32_t sa[FM];
 #pragma unroll
@@ -196,50 +279,67 @@ struct BlockGemm {
       sa[i] = *(const lds_u32_t*)(lb + B_BYTES + (wm * TM + i * 32 + l32) * 4);
     if constexpr (HW) {
       const uint32_t sb = sb_raw & 0xffu;
+      i32x8_t a[2][FM], b[2][FN];
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        i32x8_t a[FM], b[FN];
+      for (int j = 0; j < FN; ++j) b[0][j] = b_frag(j, 0);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) a[i] = a_frag(i, kk);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) b[j] = b_frag(j, kk);
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                b[j], a[i], acc[i][j], 0, 0, 0, (int)sb, 0, (int)sa[i]);
-      }
+      for (int i = 0; i < FM; ++i) a[0][i] = a_frag(i, 0);
+      static_for<NS>([&](auto q) {
+        constexpr int Q = decltype(q)::value, NM = FM * FN, NL = FM + FN;
+        constexpr int kk = Q / NM, R = Q % NM, i = R / FN, j = R % FN;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            b[kk][j], a[kk][i], acc[i][j], 0, 0, 0, (int)sb, 0, (int)sa[i]);
+        slot_dma(q);
+        if constexpr (kk == 0)
+          static_for_range<R * NL / NM, (R + 1) * NL / NM>([&](auto x) {
+            constexpr int X = decltype(x)::value;
+            if constexpr (X < FN) b[1][X] = b_frag(X, 1);
+            else a[1][X - FN] = a_frag(X - FN, 1);
+          });
+        __builtin_amdgcn_sched_barrier(0);
+      });
     } else {
       const float fb = sb_f32 ? __builtin_bit_cast(float, sb_raw) : e8m0_value(sb_raw & 0xffu);
-      i32x8_t b[2][FN];
+      float f[FM];
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
+      for (int i = 0; i < FM; ++i)
+        f[i] = (c.sa_f32 ? __builtin_bit_cast(float, sa[i]) : e8m0_value(sa[i])) * fb;
+      i32x8_t a[2], b[2][FN];  // one row fragment of A at a time
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) b[kk][j] = b_frag(j, kk);
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const float f = (sa_f32 ? __builtin_bit_cast(float, sa[i]) : e8m0_value(sa[i])) * fb;
-        const i32x8_t a[2] = {a_frag(i, 0), a_frag(i, 1)};
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          f32x16_t p = {};
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {
-            if constexpr (MODE == MODE_EXACT) {
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-                p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(b[kk][j], s), widen(a[kk], s), p,
-                                                            0, 0, 0);
-            } else {
-              p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[kk][j], a[kk], p, 0, 0, 0, 0x7f,
-                                                                  0, 0x7f);
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(f, p[e], acc[i][j][e]);
-        }
+        a[kk] = a_frag(0, kk);
       }
+      f32x16_t p[2];
+      auto add_half = [&](auto tt, auto half) {  // half of sub-tile t's scaled sums
+        constexpr int t = decltype(tt)::value, h = decltype(half)::value;
+#pragma unroll
+        for (int e = 8 * h; e < 8 * h + 8; ++e)
+          acc[t / FN][t % FN][e] = __builtin_fmaf(f[t / FN], p[t & 1][e], acc[t / FN][t % FN][e]);
+      };
+      static_for<NS>([&](auto q) {
+        constexpr int Q = decltype(q)::value, t = Q / 2, kk = Q % 2, i = t / FN, j = t % FN;
+        f32x16_t& s = p[t & 1];
+        if constexpr (kk == 0) s = f32x16_t{};
+        if constexpr (MODE == MODE_EXACT) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(b[kk][j], u), widen(a[kk], u),
+                                                        s, 0, 0, 0);
+        } else {
+          s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[kk][j], a[kk], s, 0, 0, 0, 0,
+                                                              0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (i + 1 < FM && j == FN - 1) a[kk] = a_frag(i + 1, kk);
+        slot_dma(q);
+        if constexpr (t > 0)
+          add_half(std::integral_constant<int, t - 1>{}, std::integral_constant<int, kk>{});
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      add_half(std::integral_constant<int, FM * FN - 1>{}, std::integral_constant<int, 0>{});
+      add_half(std::integral_constant<int, FM * FN - 1>{}, std::integral_constant<int, 1>{});
     }
   }
 
@@ -286,6 +386,7 @@ struct BlockGemm {
     c.sa = a.sa + arow * a.ldsa * (c.sa_f32 ? 4 : 1);
     c.ldb = a.ldb;
     c.K = a.K;
+    c.kt1 = kt1;
     c.wave = wave;
     // the block column of this wave's columns (kept inside N for waves past it)
     const uint32_t wcol = n0 + wn * TN < a.N ? n0 + wn * TN : a.N - 1;
@@ -294,25 +395,29 @@ struct BlockGemm {
     const uint8_t* sb = a.sb + ((int64_t)g * a.strideSB +
                                 (int64_t)(wcol / kScaleBlock) * (TB ? a.ldsb : 1)) *
                                    (sb_f32 ? 4 : 1);
+    c.lda32 = (uint32_t)a.lda;
+    c.ldb32 = (uint32_t)a.ldb;
     Lanes ln;
+    const uint32_t last = a.K & 127u;  // K rows of a partial last stage
+    constexpr int LPR = TB ? 8 : BN / 16;  // lanes per row of B
+    ln.a_row = (lane >> 3) * c.lda32;
+    ln.a_ch = (lane & 7u) ^ (lane >> 3);
+    ln.b_row = (lane / LPR) * c.ldb32;
+    ln.b_ch = (lane % LPR) ^ (TB ? lane >> 3 : swz_b(lane / LPR));
+    ln.inside = ln.tail = 0;
 #pragma unroll
-    for (int i = 0; i < A_IPW; ++i) {
-      const uint32_t r = (wave * A_IPW + i) * 8 + (lane >> 3), ch = (lane & 7u) ^ swz(r);
-      ln.a_k[i] = ch * 16;
-      ln.a_off[i] = r < rows_left ? r * (uint32_t)a.lda + ch * 16 : kOob;
+    for (int x = 0; x < A_IPW; ++x) {
+      const uint32_t r = (wave * A_IPW + x) * 8 + (lane >> 3), ch = ln.a_ch ^ a_xor(wave, x);
+      if (r < rows_left) ln.inside |= 1u << x;
+      if (r < rows_left && ch * 16 < last) ln.tail |= 1u << x;
     }
 #pragma unroll
-    for (int i = 0; i < B_IPW; ++i) {
-      if constexpr (TB) {
-        const uint32_t r = (wave * B_IPW + i) * 8 + (lane >> 3), ch = (lane & 7u) ^ swz(r);
-        ln.b_k[i] = ch * 16;
-        ln.b_off[i] = r < cols_left ? r * (uint32_t)a.ldb + ch * 16 : kOob;
-      } else {
-        const uint32_t byte = (wave * B_IPW + i) * 1024 + lane * 16;
-        const uint32_t k = byte / BN, ch = ((byte % BN) / 16) ^ swz_b(k);
-        ln.b_k[i] = k;
-        ln.b_off[i] = ch * 16 < cols_left ? k * (uint32_t)a.ldb + ch * 16 : kOob;
-      }
+    for (int x = 0; x < B_IPW; ++x) {
+      const uint32_t r = (wave * B_IPW + x) * RPB + lane / LPR, ch = ln.b_ch ^ b_xor(wave, x);
+      const uint32_t k = TB ? ch * 16 : r;
+      const bool in = TB ? r < cols_left : ch * 16 < cols_left;
+      if (in) ln.inside |= 1u << (A_IPW + x);
+      if (in && k < last) ln.tail |= 1u << (A_IPW + x);
     }
     const uint32_t srow = wave * 64 + lane;
     ln.s_off = wave < (uint32_t)SA_N && srow < rows_left
@@ -328,20 +433,24 @@ struct BlockGemm {
 
     // ---- K loop: at the top of a step stage kt must have landed and the
     // STAGES - 2 stages behind it may still be in flight
-    for (uint32_t s = 0; s < (uint32_t)STAGES - 1; ++s)
-      if (kt0 + s < kt1) issue(c, ln, kt0 + s, s);
+    for (uint32_t s = 0; s < (uint32_t)STAGES - 1; ++s) {
+      const Stage st = stage(c, ln, kt0 + s, s);
+      dma_scales(c, ln, st, kt0 + s);
+      static_for<ND>([&](auto x) { dma_one<decltype(x)::value>(c, ln, st); });
+    }
     uint32_t buf = 0;
     uint32_t sb_raw = kt0 < kt1 ? scalar_dword(sb + kt0 * sb_step) : 0u;
     for (uint32_t kt = kt0; kt < kt1; ++kt) {
-      if (kt + STAGES - 1 <= kt1) wait_vm<(STAGES - 2) * LPS>(); else wait_vm<0>();
+      wait_vm<(STAGES - 2) * LPS>();
       barrier_lds();
       const uint32_t nb = buf == 0 ? STAGES - 1 : buf - 1;  // the buffer read in the last step
-      if (kt + STAGES - 1 < kt1) issue(c, ln, kt + STAGES - 1, nb);
+      const Stage next = stage(c, ln, kt + STAGES - 1, nb);
+      dma_scales(c, ln, next, kt + STAGES - 1);
       const uint32_t sb_now = sb_raw;
-      if (kt + 1 < kt1) sb_raw = scalar_dword(sb + (kt + 1) * sb_step);
+      sb_raw = scalar_dword(sb + (kt + 1 < kt1 ? kt + 1 : kt) * sb_step);
       lds_t* base = lds() + buf * STAGE_BYTES;
       if (kt + 1 == a.nk && (a.K & 15u)) clear_tail(base, a.K & 127u);
-      compute(acc, base, wm, wn, sb_now, c.sa_f32 != 0, sb_f32);
+      compute(acc, base, wm, wn, sb_now, sb_f32, c, ln, next);
       buf = buf + 1 == STAGES ? 0 : buf + 1;
     }
     // ---- every wave is done with the stages: their LDS holds the strips
