@@ -24,18 +24,6 @@ __device__ __forceinline__ float e8m0_value(uint32_t e) {
   return __builtin_bit_cast(float, bits);
 }
 
-// A wave-uniform scale through the scalar cache: a byte is cut out of the
-// aligned dword that holds it (which never leaves the byte's page), so that
-// no vector load joins the DMA instructions counted in vmcnt.
-__device__ __forceinline__ uint32_t scalar_dword(const uint8_t* p) {
-  const uint64_t a = (uint64_t)(uintptr_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-  const uint64_t u = ((uint64_t)hi << 32) | lo;
-  const uint32_t w = *(const __attribute__((address_space(4))) uint32_t*)(u & ~(uint64_t)3);
-  return w >> (8u * (lo & 3u));
-}
-
 // Groups of stacked rows, in LDS: each group's first task and first row, and
 // the totals behind the last.
 struct RowGroups {

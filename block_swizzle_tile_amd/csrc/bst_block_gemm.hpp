@@ -56,18 +56,22 @@ struct BlockGemm {
   static constexpr int A_IPW = A_BYTES / 1024 / NW, B_IPW = B_BYTES / 1024 / NW;
   static constexpr int NCH = BN / 16;  // 16-byte chunks of a K row of B (TB = 0)
   static constexpr uint32_t BSWZ = pow2_block(NCH) - 1;
-  // A's scales: one dword per row, 64 rows per instruction, one instruction
-  // per wave at most; waves past them load nothing into a spare area, so
-  // that every wave has the same count in flight
+  // Scales ride with the stage, one DMA instruction per wave: waves below
+  // SA_N take A's (a dword per row, 64 rows each), wave SA_N takes B's (a
+  // dword per block of columns), and any further waves load nothing into a
+  // spare area, so that every wave has the same count in flight.  (Scalar
+  // loads of B's scale cost a cache miss per stage that every LDS read of the
+  // stage waits for, since they share a counter: 0.6 us a stage.)
   static constexpr int SA_N = (BM + 63) / 64;
   static constexpr int SA_BYTES = SA_N * 256;
-  static constexpr int SPARE = SA_N < NW ? 256 : 0;
+  static constexpr int SB_BYTES = 256;
+  static constexpr int SPARE = SA_N + 1 < NW ? 256 : 0;
   static constexpr int LPS = A_IPW + B_IPW + 1;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SPARE;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES + SPARE;
   static constexpr int LDS_BYTES = STAGES * STAGE_BYTES;
 
   static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "whole DMA waves");
-  static_assert(SA_N <= NW, "one scale instruction per wave");
+  static_assert(SA_N < NW, "one scale instruction per wave");
   static_assert(TM % 32 == 0 && TN % 32 == 0 && 128 % TN == 0, "wave tile");
   static_assert(NW * Strip<TN>::BYTES <= LDS_BYTES, "the epilogue's strips fit");
   static_assert((STAGES - 1) * LPS < 64, "vmcnt holds 6 bits");
@@ -107,10 +111,11 @@ struct BlockGemm {
   }
 
   struct Src {
-    const uint8_t *a, *b, *sa;  // panels of the task at K = 0
-    int64_t ldb;
+    const uint8_t *a, *b;  // panels of the task at K = 0
+    const uint8_t* s;      // the scales this wave loads, at K = 0
+    int64_t ldb, s_step;   // s_step: bytes from one K block's scales to the next's
     uint32_t lda32, ldb32;
-    uint32_t K, kt1, sa_f32, wave;
+    uint32_t K, kt1, s_f32, wave;
   };
 
   // Where one stage's DMA reads and writes.
@@ -152,12 +157,15 @@ struct BlockGemm {
   }
   __device__ static __forceinline__ void dma_scales(const Src& c, const Lanes& ln, const Stage& st,
                                                     uint32_t kt) {
-    lds_t* dst = st.base + A_BYTES + B_BYTES + (c.wave < (uint32_t)SA_N ? c.wave * 256u : SA_BYTES);
+    // A's areas, B's and the spare one follow each other in wave order
+    constexpr uint32_t spare = SPARE ? SA_N + 1 : SA_N;
+    lds_t* dst = st.base + A_BYTES + B_BYTES + (c.wave < spare ? c.wave : spare) * 256u;
     const uint32_t v = kt < c.kt1 ? ln.s_off : kOob;
-    if (c.sa_f32)
-      dma4(make_desc(c.sa + (uint64_t)kt * 4u), dst, v, 0u);
+    const u32x4_t d = make_desc(c.s + (int64_t)kt * c.s_step);
+    if (c.s_f32)
+      dma4(d, dst, v, 0u);
     else
-      dma1(make_desc(c.sa + kt), dst, v);
+      dma1(d, dst, v);
   }
 
   // K % 16 != 0: the last chunk of a row holds bytes past K, which may be
@@ -250,8 +258,8 @@ struct BlockGemm {
   // half of the 16 multiply-adds of the sub-tile before, which the vector unit
   // does while the matrix unit works on this one.
   __device__ static __forceinline__ void compute(f32x16_t (&acc)[FM][FN], const lds_t* base,
-                                                 uint32_t wm, uint32_t wn, uint32_t sb_raw,
-                                                 bool sb_f32, const Src& c, const Lanes& ln,
+                                                 uint32_t wm, uint32_t wn, bool sa_f32, bool sb_f32,
+                                                 const Src& c, const Lanes& ln,
                                                  const Stage& next) {
     const uint32_t l32 = threadIdx.x & 31u;
     const lds_t* lb = base + A_BYTES;
@@ -277,8 +285,11 @@ struct BlockGemm {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
       sa[i] = *(const lds_u32_t*)(lb + B_BYTES + (wm * TM + i * 32 + l32) * 4);
+    // the block of this wave's columns: the tile starts inside a block only
+    // if it is narrower than one, and then holds one
+    const uint32_t sb_raw = *(const lds_u32_t*)(lb + B_BYTES + SA_BYTES + (wn * TN / kScaleBlock) * 4);
     if constexpr (HW) {
-      const uint32_t sb = sb_raw & 0xffu;
+      const uint32_t sb = sb_raw;
       i32x8_t a[2][FM], b[2][FN];
 #pragma unroll
       for (int j = 0; j < FN; ++j) b[0][j] = b_frag(j, 0);
@@ -299,11 +310,11 @@ struct BlockGemm {
         __builtin_amdgcn_sched_barrier(0);
       });
     } else {
-      const float fb = sb_f32 ? __builtin_bit_cast(float, sb_raw) : e8m0_value(sb_raw & 0xffu);
+      const float fb = sb_f32 ? __builtin_bit_cast(float, sb_raw) : e8m0_value(sb_raw);
       float f[FM];
 #pragma unroll
       for (int i = 0; i < FM; ++i)
-        f[i] = (c.sa_f32 ? __builtin_bit_cast(float, sa[i]) : e8m0_value(sa[i])) * fb;
+        f[i] = (sa_f32 ? __builtin_bit_cast(float, sa[i]) : e8m0_value(sa[i])) * fb;
       i32x8_t a[2], b[2][FN];  // one row fragment of A at a time
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
@@ -382,19 +393,23 @@ struct BlockGemm {
     Src c;
     c.a = a.A + arow * a.lda;
     c.b = a.B + (int64_t)g * a.strideB + (TB ? (int64_t)n0 * a.ldb : (int64_t)n0);
-    c.sa_f32 = HW ? 0u : a.sa_f32;
-    c.sa = a.sa + arow * a.ldsa * (c.sa_f32 ? 4 : 1);
     c.ldb = a.ldb;
     c.K = a.K;
     c.kt1 = kt1;
     c.wave = wave;
-    // the block column of this wave's columns (kept inside N for waves past it)
-    const uint32_t wcol = n0 + wn * TN < a.N ? n0 + wn * TN : a.N - 1;
-    const bool sb_f32 = !HW && a.sb_f32;
-    const int64_t sb_step = (TB ? 1 : a.ldsb) * (sb_f32 ? 4 : 1);
-    const uint8_t* sb = a.sb + ((int64_t)g * a.strideSB +
-                                (int64_t)(wcol / kScaleBlock) * (TB ? a.ldsb : 1)) *
-                                   (sb_f32 ? 4 : 1);
+    // the scales this wave loads: A's rows, or the tile's blocks of columns
+    const bool sa_f32 = !HW && a.sa_f32, sb_f32 = !HW && a.sb_f32;
+    const bool for_a = wave < (uint32_t)SA_N;
+    c.s_f32 = for_a ? sa_f32 : sb_f32;
+    const int64_t ss = c.s_f32 ? 4 : 1;
+    const uint32_t nb = n0 / kScaleBlock, nbs = (a.N + kScaleBlock - 1) / kScaleBlock - nb;
+    if (for_a) {
+      c.s = a.sa + arow * a.ldsa * ss;
+      c.s_step = ss;
+    } else {
+      c.s = a.sb + ((int64_t)g * a.strideSB + (int64_t)nb * (TB ? a.ldsb : 1)) * ss;
+      c.s_step = (TB ? 1 : a.ldsb) * ss;
+    }
     c.lda32 = (uint32_t)a.lda;
     c.ldb32 = (uint32_t)a.ldb;
     Lanes ln;
@@ -419,9 +434,11 @@ struct BlockGemm {
       if (in) ln.inside |= 1u << (A_IPW + x);
       if (in && k < last) ln.tail |= 1u << (A_IPW + x);
     }
-    const uint32_t srow = wave * 64 + lane;
-    ln.s_off = wave < (uint32_t)SA_N && srow < rows_left
-                   ? srow * (uint32_t)a.ldsa * (c.sa_f32 ? 4u : 1u) : kOob;
+    if (for_a)
+      ln.s_off = wave * 64 + lane < rows_left ? (wave * 64 + lane) * (uint32_t)(a.ldsa * ss) : kOob;
+    else
+      ln.s_off = wave == (uint32_t)SA_N && lane < (BN + 127) / 128 && lane < nbs
+                     ? lane * (uint32_t)((TB ? a.ldsb : 1) * ss) : kOob;
 
     f32x16_t acc[FM][FN];
 #pragma unroll
@@ -439,18 +456,15 @@ struct BlockGemm {
       static_for<ND>([&](auto x) { dma_one<decltype(x)::value>(c, ln, st); });
     }
     uint32_t buf = 0;
-    uint32_t sb_raw = kt0 < kt1 ? scalar_dword(sb + kt0 * sb_step) : 0u;
     for (uint32_t kt = kt0; kt < kt1; ++kt) {
       wait_vm<(STAGES - 2) * LPS>();
       barrier_lds();
       const uint32_t nb = buf == 0 ? STAGES - 1 : buf - 1;  // the buffer read in the last step
       const Stage next = stage(c, ln, kt + STAGES - 1, nb);
       dma_scales(c, ln, next, kt + STAGES - 1);
-      const uint32_t sb_now = sb_raw;
-      sb_raw = scalar_dword(sb + (kt + 1 < kt1 ? kt + 1 : kt) * sb_step);
       lds_t* base = lds() + buf * STAGE_BYTES;
       if (kt + 1 == a.nk && (a.K & 15u)) clear_tail(base, a.K & 127u);
-      compute(acc, base, wm, wn, sb_now, sb_f32, c, ln, next);
+      compute(acc, base, wm, wn, sa_f32, sb_f32, c, ln, next);
       buf = buf + 1 == STAGES ? 0 : buf + 1;
     }
     // ---- every wave is done with the stages: their LDS holds the strips
