@@ -38,8 +38,15 @@ _SCALE = {torch.float32: F32, torch.uint8: E8M0, torch.float8_e8m0fnu: E8M0}
 _CODES = torch.float8_e4m3fn
 
 
-@functools.lru_cache(maxsize=None)
+_L = None
+
+
 def _bound():
+    return _L or _bind()
+
+
+def _bind():
+    global _L
     L = lib()
     i64, i32, p, st = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int
     sz, sp = ctypes.c_size_t, ctypes.POINTER(Sched)
@@ -57,11 +64,14 @@ def _bound():
         getattr(L, n).restype = st
     L.bst_block_workspace_bytes.argtypes = [st, i64, i64, i64, i64, sp]
     L.bst_block_workspace_bytes.restype = sz
+    _L = L
     return L
 
 
-def _cdiv(a, b):
-    return -(-a // b)
+# The calls below run in a few microseconds, so their checks use integers (device indices, raw
+# stream handles) rather than torch's device and stream objects.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _kind(t, what):
@@ -71,22 +81,23 @@ def _kind(t, what):
     return k
 
 
-def _mat(t, what, shape, dims=2, pad=1):
+def _pitch(t, what, shape, pad=1):
     """Pitch of a row-major matrix (or of each of a stack); one row has any pitch, so the least
     legal one (a multiple of pad) is given for it."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
+    st = t.stride()
     cols = shape[-1]
-    if cols > 1 and t.stride(-1) != 1:
+    if st[-1] != 1 and cols > 1:
         raise ValueError("%s: innermost dimension must be contiguous" % what)
-    if shape[-2] <= 1:
-        return _cdiv(cols, pad) * pad
-    return t.stride(-2)
+    return st[-2] if shape[-2] > 1 else -(-cols // pad) * pad
 
 
-def _codes(t, what):
-    if t.dtype != _CODES:
+def _codes(t, what, dims):
+    if t.dtype is not _CODES:
         raise TypeError("%s: expected float8_e4m3fn codes, got %s" % (what, t.dtype))
+    if t.dim() != dims:
+        raise ValueError("%s must have %d dimensions" % (what, dims))
 
 
 def _scale_kind(t, what):
@@ -97,34 +108,24 @@ def _scale_kind(t, what):
     return k
 
 
-def _device(first, *rest):
-    d = first.device
-    if d.type != "cuda":
+def _device(*tensors):
+    """Index of the one GPU that holds all tensors."""
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != d:
+            raise ValueError("operands are on different devices")
+    if d < 0:
         raise ValueError("operands must be GPU tensors")
-    for t in rest:
-        if t is not None and t.device != d:
-            raise ValueError("operands are on different devices (%s, %s)" % (d, t.device))
     return d
 
 
-def _guard(fn):
-    """Runs fn with its first tensor's device current: kernels launch on the current device."""
+def _elsewhere(fn):
+    """fn(device index, ...) run with that device current: kernels launch on the current device."""
     @functools.wraps(fn)
-    def call(first, *args, **kwargs):
-        d = first.device
-        if d.type == "cuda" and d.index != torch.cuda.current_device():
-            with torch.cuda.device(d):
-                return fn(first, *args, **kwargs)
-        return fn(first, *args, **kwargs)
+    def call(d, *args):
+        with torch.cuda.device(d):
+            return fn(d, *args)
     return call
-
-
-def _stream(d):
-    return torch.cuda.current_stream(d).cuda_stream
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
 
 
 def _s(s):
@@ -138,25 +139,59 @@ def block_workspace_bytes(kind, count, M, N, K, sched=None):
 
 
 @functools.lru_cache(maxsize=4096)
-def _ws_bytes(device, kind, count, M, N, K):
+def _ws_bytes(d, kind, count, M, N, K):
     return block_workspace_bytes(kind, count, M, N, K)
 
 
-def _workspace(ws, d, kind, count, M, N, K, sched):
+def _workspace(ws, first, d, kind, count, M, N, K, sched):
+    """(pointer, bytes, the tensor that holds them): the caller's, or a new one where needed."""
     if ws is not None:
-        if ws.device != d:
+        if ws.get_device() != d:
             raise ValueError("the workspace is on another device")
         if not ws.is_contiguous():
             raise ValueError("the workspace must be contiguous")
-        return ws, ws.numel() * ws.element_size()
-    n = (_ws_bytes(d.index, kind, count, M, N, K) if sched is None
+        return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+    n = (_ws_bytes(d, kind, count, M, N, K) if sched is None
          else block_workspace_bytes(kind, count, M, N, K, sched))
     if n == 0:
-        return None, 0
-    return torch.empty(n, dtype=torch.uint8, device=d), n
+        return None, 0, None
+    ws = first.new_empty(n, dtype=torch.uint8)
+    return ws.data_ptr(), n, ws
 
 
-@_guard
+def _quant(d, X, Q, scale, block_rows):
+    if X.dim() != 2:
+        raise ValueError("X must be a matrix")
+    M, K = X.shape
+    kb = -(-K // 128)
+    if block_rows == 1:
+        sshape = (M, kb)
+    elif block_rows == 128:
+        sshape = (-(-M // 128), kb)
+    else:
+        raise ValueError("block_rows must be 1 or 128")
+    kind = _kind(X.dtype, "X")
+    ldx = _pitch(X, "X", (M, K))
+    if Q is None:
+        if K % 16 == 0:
+            Q, ldq = X.new_empty((M, K), dtype=_CODES), K
+        else:
+            ldq = -(-K // 16) * 16
+            Q = X.new_empty((M, ldq), dtype=_CODES)[:, :K]
+    else:
+        _codes(Q, "Q", 2)
+        ldq = _pitch(Q, "Q", (M, K))
+    if scale is None:
+        scale, lds = X.new_empty(sshape, dtype=torch.uint8), kb
+    else:
+        if _scale_kind(scale, "scale") != E8M0:
+            raise TypeError("quant_block writes E8M0 scales")
+        lds = _pitch(scale, "scale", sshape)
+    check(_bound().bst_quant_block(kind, M, K, block_rows, X.data_ptr(), ldx, Q.data_ptr(), ldq,
+                                   scale.data_ptr(), lds, _current_stream(d)))
+    return Q, scale
+
+
 def quant_block(X, Q=None, scale=None, *, block_rows=1):
     """8-bit codes and E8M0 scales of X [M][K] (bf16, fp16 or fp32): (Q, scale).
 
@@ -165,169 +200,175 @@ def quant_block(X, Q=None, scale=None, *, block_rows=1):
     16 != 0 it is a view of a wider matrix.  Rounding is to nearest even under the smallest
     power-of-two scale that holds the block's largest finite magnitude; infinities and NaN become
     NaN (bst_quant_block)."""
-    if X.dim() != 2:
-        raise ValueError("X must be a matrix")
-    M, K = X.shape
-    kind = _kind(X.dtype, "X")
     d = _device(X, Q, scale)
-    if block_rows not in (1, 128):
-        raise ValueError("block_rows must be 1 or 128")
-    ldx = _mat(X, "X", (M, K))
-    if Q is None:
-        if K % 16 == 0:
-            Q = torch.empty((M, K), dtype=_CODES, device=d)
-        else:
-            Q = torch.empty((M, _cdiv(K, 16) * 16), dtype=_CODES, device=d)[:, :K]
-    else:
-        _codes(Q, "Q")
-    sshape = (M if block_rows == 1 else _cdiv(M, 128), _cdiv(K, 128))
-    if scale is None:
-        scale = torch.empty(sshape, dtype=torch.uint8, device=d)
-    elif _scale_kind(scale, "scale") != E8M0:
-        raise TypeError("quant_block writes E8M0 scales")
-    check(_bound().bst_quant_block(kind, M, K, block_rows, X.data_ptr(), ldx, Q.data_ptr(),
-                                   _mat(Q, "Q", (M, K)), scale.data_ptr(),
-                                   _mat(scale, "scale", sshape), _stream(d)))
-    return Q, scale
+    if d != _current_device():
+        return _elsewhere(_quant)(d, X, Q, scale, block_rows)
+    return _quant(d, X, Q, scale, block_rows)
 
 
-@_guard
-def dequant_block(Q, scale, X=None, *, out_dtype=None, block_rows=1):
-    """The matrix that codes Q and scales stand for, in out_dtype (bf16 by default; bf16, fp16 or
-    fp32); finite values past the type's range give its largest (bst_dequant_block)."""
-    _codes(Q, "Q")
-    if Q.dim() != 2:
-        raise ValueError("Q must be a matrix")
+def _dequant(d, Q, scale, X, out_dtype, block_rows):
+    _codes(Q, "Q", 2)
     M, K = Q.shape
-    d = _device(Q, scale, X)
-    if block_rows not in (1, 128):
+    kb = -(-K // 128)
+    if block_rows == 1:
+        sshape = (M, kb)
+    elif block_rows == 128:
+        sshape = (-(-M // 128), kb)
+    else:
         raise ValueError("block_rows must be 1 or 128")
     sk = _scale_kind(scale, "scale")
     if X is None:
-        X = torch.empty((M, K), dtype=out_dtype or torch.bfloat16, device=d)
-    sshape = (M if block_rows == 1 else _cdiv(M, 128), _cdiv(K, 128))
+        X, ldx = Q.new_empty((M, K), dtype=out_dtype or torch.bfloat16), K
+    else:
+        ldx = _pitch(X, "X", (M, K))
     check(_bound().bst_dequant_block(_kind(X.dtype, "X"), M, K, block_rows, Q.data_ptr(),
-                                     _mat(Q, "Q", (M, K)), sk, scale.data_ptr(),
-                                     _mat(scale, "scale", sshape), X.data_ptr(),
-                                     _mat(X, "X", (M, K)), _stream(d)))
+                                     _pitch(Q, "Q", (M, K)), sk, scale.data_ptr(),
+                                     _pitch(scale, "scale", sshape), X.data_ptr(), ldx,
+                                     _current_stream(d)))
     return X
 
 
+def dequant_block(Q, scale, X=None, *, out_dtype=None, block_rows=1):
+    """The matrix that codes Q and scales stand for, in out_dtype (bf16 by default; bf16, fp16 or
+    fp32); finite values past the type's range give its largest (bst_dequant_block)."""
+    d = _device(Q, scale, X)
+    if d != _current_device():
+        return _elsewhere(_dequant)(d, Q, scale, X, out_dtype, block_rows)
+    return _dequant(d, Q, scale, X, out_dtype, block_rows)
+
+
 def _product(A, B, scale_a, scale_b, trans_b, lead):
-    _codes(A, "A")
-    _codes(B, "B")
-    if A.dim() != 2 or B.dim() != 2 + len(lead):
-        raise ValueError("A must be a matrix, B %s" % ("a stack of matrices" if lead else "a matrix"))
+    _codes(A, "A", 2)
+    _codes(B, "B", 2 + len(lead))
     M, K = A.shape
     N = B.shape[-2] if trans_b else B.shape[-1]
-    kb, nb = _cdiv(K, 128), _cdiv(N, 128)
-    lda = _mat(A, "A", (M, K), pad=16)
-    ldb = _mat(B, "B", (*lead, N, K) if trans_b else (*lead, K, N), pad=16)
-    ldsa = _mat(scale_a, "scale_a", (M, kb))
-    ldsb = _mat(scale_b, "scale_b", (*lead, nb, kb) if trans_b else (*lead, kb, nb))
-    return (M, N, K, lda, ldb, ldsa, ldsb, _scale_kind(scale_a, "scale_a"),
-            _scale_kind(scale_b, "scale_b"))
+    kb, nb = -(-K // 128), -(-N // 128)
+    return (M, N, K, _pitch(A, "A", (M, K), 16),
+            _pitch(B, "B", (*lead, N, K) if trans_b else (*lead, K, N), 16),
+            _pitch(scale_a, "scale_a", (M, kb)),
+            _pitch(scale_b, "scale_b", (*lead, nb, kb) if trans_b else (*lead, kb, nb)),
+            _scale_kind(scale_a, "scale_a"), _scale_kind(scale_b, "scale_b"))
 
 
-@_guard
+def _gemm(d, A, B, scale_a, scale_b, C, trans_b, out_dtype, sched, workspace):
+    M, N, K, lda, ldb, ldsa, ldsb, ka, kb = _product(A, B, scale_a, scale_b, trans_b, ())
+    if C is None:
+        C, ldc = A.new_empty((M, N), dtype=out_dtype or torch.bfloat16), N
+    else:
+        ldc = _pitch(C, "C", (M, N))
+    wp, wn, _keep = _workspace(workspace, A, d, 0, 1, M, N, K, sched)
+    check(_bound().bst_gemm_block_scaled(_kind(C.dtype, "C"), trans_b, M, N, K, A.data_ptr(), lda,
+                                         ka, scale_a.data_ptr(), ldsa, B.data_ptr(), ldb, kb,
+                                         scale_b.data_ptr(), ldsb, C.data_ptr(), ldc, _s(sched), wp,
+                                         wn, _current_stream(d)))
+    return C
+
+
 def gemm_block_scaled(A, B, scale_a, scale_b, C=None, *, trans_b=False, out_dtype=None, sched=None,
                       workspace=None):
     """C = A @ B of two 8-bit matrices with block scales (fp32 sums; bf16 out by default).
 
     A [M][K] with scale_a [M][ceil(K/128)]; B [K][N] with scale_b [ceil(K/128)][ceil(N/128)], or
     with trans_b B [N][K] and scale_b [ceil(N/128)][ceil(K/128)] (bst_gemm_block_scaled)."""
-    trans_b = bool(trans_b)
     d = _device(A, B, scale_a, scale_b, C)
-    M, N, K, lda, ldb, ldsa, ldsb, ka, kb = _product(A, B, scale_a, scale_b, trans_b, ())
-    if C is None:
-        C = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=d)
-    ws, wsb = _workspace(workspace, d, 0, 1, M, N, K, sched)
-    check(_bound().bst_gemm_block_scaled(_kind(C.dtype, "C"), trans_b, M, N, K, A.data_ptr(), lda,
-                                         ka, scale_a.data_ptr(), ldsa, B.data_ptr(), ldb, kb,
-                                         scale_b.data_ptr(), ldsb, C.data_ptr(),
-                                         _mat(C, "C", (M, N)), _s(sched), _p(ws), wsb, _stream(d)))
-    return C
+    args = (d, A, B, scale_a, scale_b, C, bool(trans_b), out_dtype, sched, workspace)
+    return _gemm(*args) if d == _current_device() else _elsewhere(_gemm)(*args)
 
 
 def _groups(group_m):
-    if group_m.dtype != torch.int32 or group_m.dim() != 1 or not group_m.is_contiguous():
+    if group_m.dtype is not torch.int32 or group_m.dim() != 1 or not group_m.is_contiguous():
         raise TypeError("group_m must be a contiguous int32 vector")
     return group_m.numel()
 
 
-@_guard
+def _grouped(d, A, B, group_m, scale_a, scale_b, C, trans_b, out_dtype, sched):
+    G = _groups(group_m)
+    M, N, K, lda, ldb, ldsa, ldsb, ka, kb = _product(A, B, scale_a, scale_b, trans_b, (G,))
+    if C is None:
+        C, ldc = A.new_empty((M, N), dtype=out_dtype or torch.bfloat16), N
+    else:
+        ldc = _pitch(C, "C", (M, N))
+    check(_bound().bst_grouped_gemm_block_scaled(
+        _kind(C.dtype, "C"), trans_b, G, group_m.data_ptr(), M, N, K, A.data_ptr(), lda, ka,
+        scale_a.data_ptr(), ldsa, B.data_ptr(), ldb, B.stride(0) if G > 1 else 0, kb,
+        scale_b.data_ptr(), ldsb, scale_b.stride(0) if G > 1 else 0, C.data_ptr(), ldc, _s(sched),
+        _current_stream(d)))
+    return C
+
+
 def grouped_gemm_block_scaled(A, B, group_m, scale_a, scale_b, C=None, *, trans_b=False,
                               out_dtype=None, sched=None):
     """Groups of rows stacked along M, each times its own B[g]: group_m is a device int32 vector of
     row counts (never read on the host).  Rows of C past the last group are left as they were
     (unset in a new C) (bst_grouped_gemm_block_scaled)."""
-    trans_b = bool(trans_b)
     d = _device(A, B, group_m, scale_a, scale_b, C)
-    G = _groups(group_m)
-    M, N, K, lda, ldb, ldsa, ldsb, ka, kb = _product(A, B, scale_a, scale_b, trans_b, (G,))
-    if C is None:
-        C = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=d)
-    check(_bound().bst_grouped_gemm_block_scaled(
-        _kind(C.dtype, "C"), trans_b, G, group_m.data_ptr(), M, N, K, A.data_ptr(), lda, ka,
-        scale_a.data_ptr(), ldsa, B.data_ptr(), ldb, B.stride(0) if G > 1 else 0, kb,
-        scale_b.data_ptr(), ldsb, scale_b.stride(0) if G > 1 else 0, C.data_ptr(),
-        _mat(C, "C", (M, N)), _s(sched), _stream(d)))
-    return C
+    args = (d, A, B, group_m, scale_a, scale_b, C, bool(trans_b), out_dtype, sched)
+    return _grouped(*args) if d == _current_device() else _elsewhere(_grouped)(*args)
 
 
-def _grad_out(dW, add, out_dtype, shape, d):
+def _grad_out(Q, dW, add, out_dtype, shape):
+    """(dW, its pitch, the addend's pointer and pitch)."""
     if dW is None:
         dtype = out_dtype or (add.dtype if add is not None else torch.float32)
-        dW = torch.empty(shape, dtype=dtype, device=d)
-    if add is not None and add.dtype != dW.dtype:
+        dW, ld = Q.new_empty(shape, dtype=dtype), shape[-1]
+    else:
+        ld = _pitch(dW, "dW", shape)
+    if add is None:
+        return dW, ld, None, 0
+    if add.dtype is not dW.dtype:
         raise TypeError("add must have dW's dtype")
-    return dW
+    return dW, ld, add.data_ptr(), _pitch(add, "add", shape)
 
 
 def _grad_in(Q, scale, dY):
-    _codes(Q, "Q")
-    if Q.dim() != 2 or dY.dim() != 2:
-        raise ValueError("Q and dY must be matrices")
+    _codes(Q, "Q", 2)
+    if dY.dim() != 2:
+        raise ValueError("dY must be a matrix")
     if _scale_kind(scale, "scale") != E8M0:
         raise TypeError("activations kept in 8 bits have E8M0 scales (quant_block)")
     M, K = Q.shape
     N = dY.shape[1]
-    return (M, K, N, _mat(Q, "Q", (M, K), pad=16), _mat(scale, "scale", (M, _cdiv(K, 128))),
-            _mat(dY, "dY", (M, N)))
+    return (M, K, N, _pitch(Q, "Q", (M, K), 16), _pitch(scale, "scale", (M, -(-K // 128))),
+            _pitch(dY, "dY", (M, N)))
 
 
-@_guard
+def _grad(d, Q, scale, dY, dW, add, out_dtype, sched, workspace):
+    M, K, N, ldq, lds, ldy = _grad_in(Q, scale, dY)
+    dW, ldw, ap, lda = _grad_out(Q, dW, add, out_dtype, (K, N))
+    wp, wn, _keep = _workspace(workspace, Q, d, 1, 1, M, N, K, sched)
+    check(_bound().bst_weight_grad(_kind(dY.dtype, "dY"), _kind(dW.dtype, "dW"), M, N, K,
+                                   Q.data_ptr(), ldq, scale.data_ptr(), lds, dY.data_ptr(), ldy, ap,
+                                   lda, dW.data_ptr(), ldw, _s(sched), wp, wn, _current_stream(d)))
+    return dW
+
+
 def weight_grad(Q, scale, dY, dW=None, *, add=None, out_dtype=None, sched=None, workspace=None):
     """dW [K][N] = add + X.T @ dY for X [M][K] kept in 8 bits as quant_block made it (codes Q, E8M0
     scales) and dY [M][N] in bf16, fp16 or fp32; no operand is rounded, sums are fp32.  add: dW's
     dtype and shape, may be dW itself (gradient accumulation).  fp32 out by default
     (bst_weight_grad)."""
     d = _device(Q, scale, dY, dW, add)
+    args = (d, Q, scale, dY, dW, add, out_dtype, sched, workspace)
+    return _grad(*args) if d == _current_device() else _elsewhere(_grad)(*args)
+
+
+def _grouped_grad(d, Q, scale, dY, group_m, dW, add, out_dtype, sched, workspace):
+    G = _groups(group_m)
     M, K, N, ldq, lds, ldy = _grad_in(Q, scale, dY)
-    dW = _grad_out(dW, add, out_dtype, (K, N), d)
-    ws, wsb = _workspace(workspace, d, 1, 1, M, N, K, sched)
-    check(_bound().bst_weight_grad(
-        _kind(dY.dtype, "dY"), _kind(dW.dtype, "dW"), M, N, K, Q.data_ptr(), ldq, scale.data_ptr(),
-        lds, dY.data_ptr(), ldy, _p(add), _mat(add, "add", (K, N)) if add is not None else 0,
-        dW.data_ptr(), _mat(dW, "dW", (K, N)), _s(sched), _p(ws), wsb, _stream(d)))
+    dW, ldw, ap, lda = _grad_out(Q, dW, add, out_dtype, (G, K, N))
+    wp, wn, _keep = _workspace(workspace, Q, d, 2, G, M, N, K, sched)
+    check(_bound().bst_grouped_weight_grad(
+        _kind(dY.dtype, "dY"), _kind(dW.dtype, "dW"), G, group_m.data_ptr(), M, N, K, Q.data_ptr(),
+        ldq, scale.data_ptr(), lds, dY.data_ptr(), ldy, ap, lda,
+        add.stride(0) if add is not None and G > 1 else 0, dW.data_ptr(), ldw,
+        dW.stride(0) if G > 1 else 0, _s(sched), wp, wn, _current_stream(d)))
     return dW
 
 
-@_guard
 def grouped_weight_grad(Q, scale, dY, group_m, dW=None, *, add=None, out_dtype=None, sched=None,
                         workspace=None):
     """weight_grad over each group of rows: dW [G][K][N], group_m a device int32 vector of row
     counts; an empty group's gradient is its add (or zeros) (bst_grouped_weight_grad)."""
     d = _device(Q, scale, dY, group_m, dW, add)
-    G = _groups(group_m)
-    M, K, N, ldq, lds, ldy = _grad_in(Q, scale, dY)
-    dW = _grad_out(dW, add, out_dtype, (G, K, N), d)
-    lda = _mat(add, "add", (G, K, N)) if add is not None else 0
-    ws, wsb = _workspace(workspace, d, 2, G, M, N, K, sched)
-    check(_bound().bst_grouped_weight_grad(
-        _kind(dY.dtype, "dY"), _kind(dW.dtype, "dW"), G, group_m.data_ptr(), M, N, K, Q.data_ptr(),
-        ldq, scale.data_ptr(), lds, dY.data_ptr(), ldy, _p(add), lda,
-        add.stride(0) if add is not None and G > 1 else 0, dW.data_ptr(),
-        _mat(dW, "dW", (G, K, N)), dW.stride(0) if G > 1 else 0, _s(sched), _p(ws), wsb,
-        _stream(d)))
-    return dW
+    args = (d, Q, scale, dY, group_m, dW, add, out_dtype, sched, workspace)
+    return _grouped_grad(*args) if d == _current_device() else _elsewhere(_grouped_grad)(*args)
