@@ -133,8 +133,8 @@ def _s(s):
 
 
 def block_workspace_bytes(kind, count, M, N, K, sched=None):
-    """Workspace bytes of :func:`gemm_block_scaled` (kind 0), :func:`weight_grad` (1) or
-    :func:`grouped_weight_grad` (2, count = groups, M = rows in all) on the current device."""
+    """Workspace bytes of :func:`gemm_block_scaled` (kind 0; 3 with trans_b), :func:`weight_grad`
+    (1) or :func:`grouped_weight_grad` (2, count = groups, M = rows in all) on the current device."""
     return _bound().bst_block_workspace_bytes(kind, count, M, N, K, _s(sched))
 
 
@@ -256,7 +256,7 @@ def _gemm(d, A, B, scale_a, scale_b, C, trans_b, out_dtype, sched, workspace):
         C, ldc = A.new_empty((M, N), dtype=out_dtype or torch.bfloat16), N
     else:
         ldc = _pitch(C, "C", (M, N))
-    wp, wn, _keep = _workspace(workspace, A, d, 0, 1, M, N, K, sched)
+    wp, wn, _keep = _workspace(workspace, A, d, 3 if trans_b else 0, 1, M, N, K, sched)
     check(_bound().bst_gemm_block_scaled(_kind(C.dtype, "C"), trans_b, M, N, K, A.data_ptr(), lda,
                                          ka, scale_a.data_ptr(), ldsa, B.data_ptr(), ldb, kb,
                                          scale_b.data_ptr(), ldsb, C.data_ptr(), ldc, _s(sched), wp,

@@ -14,7 +14,7 @@ SOURCES = ["bst.hip", "inst_f16.hip", "inst_bf16.hip", "inst_i8.hip", "inst_fp8.
            "block_grad.hip"]
 HEADERS = ["bst_device.hpp", "bst_kernel_dma.hpp", "bst_instances.hpp", "bst_block.hpp",
            "bst_block_gemm.hpp", "bst_block_grad.hpp", "bst_block_quant.hpp",
-           "bst_block_instances.hpp"]
+           "bst_block_rows.hpp", "bst_block_instances.hpp"]
 DEPS = ([os.path.join(CSRC, f) for f in SOURCES + HEADERS] +
         [os.path.join(ROOT, "include", f) for f in ("bst.h", "bst_block.h")])
 LIB = os.path.join(PKG, "libbst.so")

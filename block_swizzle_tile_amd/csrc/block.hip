@@ -194,6 +194,12 @@ bst_status plan_grad(int64_t count, int64_t M, int64_t N, int64_t K, const Sched
   return plan_workspace(p, G * K, N);
 }
 
+// Products that the kernel for a few rows takes: weights stored N x K, and
+// neither a tile nor a split asked for.
+bool takes_rows(int32_t trans_b, int64_t M, const Sched& s) {
+  return trans_b && M <= 32 && s.tm == 0 && s.tn == 0 && s.split == 0;
+}
+
 bst_status check_ws(const Plan& p, const void* ws, size_t bytes) {
   if (p.ws == 0) return BST_OK;
   if (!ws || bytes < p.ws)
@@ -257,9 +263,12 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
     if (grouped && strideB % 16 != 0)
       return set_error(BST_E_ALIGN, "strideB must be a multiple of 16 bytes");
   }
+  const bool rows = !grouped && takes_rows(trans_b, M, s);
   Plan p;
-  if ((st = plan_gemm(grouped ? G : 0, M, N, K, s, p)) != BST_OK) return st;
-  if ((st = check_ws(p, ws, ws_bytes)) != BST_OK) return st;
+  if (!rows) {
+    if ((st = plan_gemm(grouped ? G : 0, M, N, K, s, p)) != BST_OK) return st;
+    if ((st = check_ws(p, ws, ws_bytes)) != BST_OK) return st;
+  }
   const int mode = c == BST_F32 ? MODE_EXACT : sa == BST_E8M0 && sb == BST_E8M0 ? MODE_E8M0 : MODE_F32;
   const BlockGemmList l = grouped ? (trans_b ? block_gemm_grouped_t() : block_gemm_grouped_n())
                                   : (trans_b ? block_gemm_plain_t() : block_gemm_plain_n());
@@ -267,7 +276,7 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
   for (int i = 0; i < l.count && !in; ++i)
     if ((uint32_t)l.begin[i].bm == p.tm && (uint32_t)l.begin[i].bn == p.tn && l.begin[i].mode == mode)
       in = l.begin + i;
-  if (!in) return set_error(BST_E_UNSUPPORTED, "no block-scaled kernel with tile %ux%u", p.tm, p.tn);
+  if (!in && !rows) return set_error(BST_E_UNSUPPORTED, "no block-scaled kernel with tile %ux%u", p.tm, p.tn);
 
   BlockGemmArgs a{};
   a.A = A;
@@ -298,6 +307,19 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
   a.sb_f32 = sb == BST_F32;
   a.ckind = (uint32_t)c;
   a.cvec = vec_rows(C, ldc, 0, out_bytes(c));
+  if (rows) {
+    const dim3 grid((uint32_t)cdiv(N, 16)), block(512);
+    const hipStream_t q = (hipStream_t)stream;
+    if (M <= 16 && mode == MODE_EXACT)
+      hipLaunchKernelGGL((block_rows_kernel<1, true>), grid, block, 0, q, a);
+    else if (M <= 16)
+      hipLaunchKernelGGL((block_rows_kernel<1, false>), grid, block, 0, q, a);
+    else if (mode == MODE_EXACT)
+      hipLaunchKernelGGL((block_rows_kernel<2, true>), grid, block, 0, q, a);
+    else
+      hipLaunchKernelGGL((block_rows_kernel<2, false>), grid, block, 0, q, a);
+    return launched(hipGetLastError(), "block-scaled product");
+  }
   if (p.split > 1) {
     a.part = static_cast<float*>(ws);
     a.pitch = p.pitch;
@@ -528,17 +550,19 @@ size_t bst_block_workspace_bytes(int kind, int64_t count, int64_t M, int64_t N, 
                                  const bst_sched* sched) {
   Sched s;
   Plan p;
-  if (kind < 0 || kind > 2) {
-    set_error(BST_E_INVAL, "workspace kind %d not in {0, 1, 2}", kind);
+  if (kind < 0 || kind > 3) {
+    set_error(BST_E_INVAL, "workspace kind %d not in {0, 1, 2, 3}", kind);
     return 0;
   }
-  if (sizes_ok(M, N, K) != BST_OK || read_sched(sched, kind == 0 ? 128 : 0, s) != BST_OK) return 0;
+  if (sizes_ok(M, N, K) != BST_OK || read_sched(sched, kind == 0 || kind == 3 ? 128 : 0, s) != BST_OK)
+    return 0;
   if (kind == 2 && (count < 1 || count > kMaxGroups)) {
     set_error(BST_E_INVAL, "group count %lld outside [1, %d]", (long long)count, kMaxGroups);
     return 0;
   }
-  const bst_status st = kind == 0 ? plan_gemm(0, M, N, K, s, p)
-                                  : plan_grad(kind == 2 ? count : 0, M, N, K, s, p);
+  if (kind == 3 && takes_rows(1, M, s)) return 0;
+  const bst_status st = kind == 0 || kind == 3 ? plan_gemm(0, M, N, K, s, p)
+                                               : plan_grad(kind == 2 ? count : 0, M, N, K, s, p);
   return st == BST_OK ? p.ws : 0;
 }
 

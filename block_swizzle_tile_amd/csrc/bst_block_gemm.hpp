@@ -47,6 +47,18 @@ __device__ __forceinline__ void dma1(const u32x4_t& desc, const lds_t* lds, uint
                : "memory");
 }
 
+// Codes of a fragment's bytes 8s .. 8s+7 as a bf16 operand.
+__device__ __forceinline__ bf16x8_t widen_codes(const i32x8_t& f, int s) {
+  u32x4_t o;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    const uint32_t w = (uint32_t)f[2 * s + d];
+    o[2 * d] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+    o[2 * d + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
+  }
+  return __builtin_bit_cast(bf16x8_t, o);
+}
+
 template <int BM, int BN, int WM, int WN, int STAGES, bool TB, int MODE, bool GROUPED>
 struct BlockGemm {
   static constexpr bool HW = MODE == MODE_E8M0;
@@ -237,19 +249,6 @@ struct BlockGemm {
     return i32x8_t{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
   }
 
-  // Codes of a fragment's bytes 8s .. 8s+7 as a bf16 operand.
-  __device__ static __forceinline__ bf16x8_t widen(const i32x8_t& f, int s) {
-    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-    u32x4_t o;
-#pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      const uint32_t w = (uint32_t)f[2 * s + d];
-      o[2 * d] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
-      o[2 * d + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
-    }
-    return __builtin_bit_cast(bf16x8_t, o);
-  }
-
   // The products of one stage, with the DMA of a later one (`next`) between
   // them.  The order is fixed by hand, one matrix instruction per slot:
   // behind each go its share of the DMA instructions (one per slot from the
@@ -336,7 +335,7 @@ struct BlockGemm {
         if constexpr (MODE == MODE_EXACT) {
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(b[kk][j], u), widen(a[kk], u),
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_codes(b[kk][j], u), widen_codes(a[kk], u),
                                                         s, 0, 0, 0);
         } else {
           s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[kk][j], a[kk], s, 0, 0, 0, 0,

@@ -7,6 +7,7 @@
 
 #include "bst_block_gemm.hpp"
 #include "bst_block_grad.hpp"
+#include "bst_block_rows.hpp"
 
 namespace bst {
 

@@ -142,9 +142,11 @@ def test_workspace(L):
     need = L.bst_block_workspace_bytes(2, 4, 2048, 128, 256, ctypes.byref(g))
     assert need == 3 * 4 * 256 * 128 * 4
     assert ggrad(L, M=2048, sched=ctypes.byref(g)) == _lib.E_WORKSPACE
-    assert L.bst_block_workspace_bytes(3, 1, 1, 1, 1, None) == 0
+    assert L.bst_block_workspace_bytes(4, 1, 1, 1, 1, None) == 0
     assert b"kind" in L.bst_last_error()
     assert L.bst_block_workspace_bytes(2, 0, 1, 1, 1, None) == 0
+    assert L.bst_block_workspace_bytes(0, 1, 1, 512, 4096, None) > 0
+    assert L.bst_block_workspace_bytes(3, 1, 1, 512, 4096, None) == 0    # few rows, weights N x K
     # a split never has an empty slice: 3 blocks of K cut 8 ways are 3 slices
     s = bst.make_sched(tile=(64, 128), split_k=8)
     assert L.bst_block_workspace_bytes(0, 1, 64, 256, 384, ctypes.byref(s)) == 3 * 64 * 256 * 4
