@@ -62,6 +62,7 @@ __device__ __forceinline__ bf16x8_t widen_codes(const i32x8_t& f, int s) {
 template <int BM, int BN, int WM, int WN, int STAGES, bool TB, int MODE, bool GROUPED>
 struct BlockGemm {
   static constexpr bool HW = MODE == MODE_E8M0;
+  static constexpr bool RING = STAGES >= 3;
   static constexpr int NW = WM * WN, NT = 64 * NW;
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
@@ -353,6 +354,147 @@ struct BlockGemm {
     }
   }
 
+  // ---- Read-ahead (RING): while a stage is multiplied, the operands of the
+  // next one are read from LDS into a second set of registers, so that no
+  // matrix instruction waits for LDS at a stage's start.  The next stage then
+  // has to have landed one step earlier, which takes a third buffer, and the
+  // second set fits only beside the accumulators of the smaller tiles.
+  struct Frags {
+    i32x8_t a[2][FM], b[2][FN];
+    uint32_t sa[FM], sb;
+  };
+  static constexpr int NL = 2 * (FM + FN);  // operand loads of a stage
+  struct Ptrs {
+    RowPtrs a;
+    typename std::conditional<TB, RowPtrs, ColPtrs>::type b;
+    const lds_t* s;
+  };
+  __device__ static __forceinline__ Ptrs ptrs(const lds_t* base, uint32_t wm, uint32_t wn) {
+    Ptrs r;
+    r.a = row_ptrs(base, wm * TM);
+    if constexpr (TB)
+      r.b = row_ptrs(base + A_BYTES, wn * TN);
+    else
+      r.b = col_ptrs(base + A_BYTES, wn);
+    r.s = base + A_BYTES + B_BYTES;
+    return r;
+  }
+  __device__ static __forceinline__ void load_scales(Frags& f, const Ptrs& r, uint32_t wm, uint32_t wn) {
+    const uint32_t l32 = threadIdx.x & 31u;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) f.sa[i] = *(const lds_u32_t*)(r.s + (wm * TM + i * 32 + l32) * 4);
+    f.sb = *(const lds_u32_t*)(r.s + SA_BYTES + (wn * TN / kScaleBlock) * 4);
+  }
+  template <int X>
+  __device__ static __forceinline__ void load_frag(Frags& f, const Ptrs& r) {
+    constexpr int kk = X / (FM + FN), x = X % (FM + FN);
+    if constexpr (x < FN) {
+      if constexpr (TB) f.b[kk][x] = rows_frag(r.b, x, kk);
+      else f.b[kk][x] = cols_frag(r.b, x, kk);
+    } else {
+      f.a[kk][x - FN] = rows_frag(r.a, x - FN, kk);
+    }
+  }
+
+  __device__ static __forceinline__ void step_ring(f32x16_t (&acc)[FM][FN], const Frags& f, Frags& n,
+                                                   const Ptrs& np, uint32_t wm, uint32_t wn,
+                                                   bool sa_f32, bool sb_f32, const Src& c,
+                                                   const Lanes& ln, const Stage& next) {
+    constexpr int NS = 2 * FM * FN;
+    auto behind = [&](auto q) {  // what rides behind slot q's matrix instruction
+      constexpr int Q = decltype(q)::value;
+      if constexpr (Q == 0) load_scales(n, np, wm, wn);
+      static_for_range<Q * NL / NS, (Q + 1) * NL / NS>(
+          [&](auto x) { load_frag<decltype(x)::value>(n, np); });
+      static_for_range<Q * ND / NS, (Q + 1) * ND / NS>(
+          [&](auto x) { dma_one<decltype(x)::value>(c, ln, next); });
+    };
+    if constexpr (HW) {
+      static_for<NS>([&](auto q) {
+        constexpr int Q = decltype(q)::value, kk = Q / (FM * FN), R = Q % (FM * FN);
+        constexpr int i = R / FN, j = R % FN;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            f.b[kk][j], f.a[kk][i], acc[i][j], 0, 0, 0, (int)f.sb, 0, (int)f.sa[i]);
+        __builtin_amdgcn_sched_barrier(0);
+        behind(q);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    } else {
+      const float fb = sb_f32 ? __builtin_bit_cast(float, f.sb) : e8m0_value(f.sb);
+      float s[FM];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const uint32_t w = f.sa[i];
+        s[i] = (sa_f32 ? __builtin_bit_cast(float, w) : e8m0_value(w)) * fb;
+      }
+      f32x16_t p[2];
+      auto add_half = [&](auto tt, auto half) {
+        constexpr int t = decltype(tt)::value, h = decltype(half)::value;
+#pragma unroll
+        for (int e = 8 * h; e < 8 * h + 8; ++e)
+          acc[t / FN][t % FN][e] = __builtin_fmaf(s[t / FN], p[t & 1][e], acc[t / FN][t % FN][e]);
+      };
+      static_for<NS>([&](auto q) {
+        constexpr int Q = decltype(q)::value, t = Q / 2, kk = Q % 2, i = t / FN, j = t % FN;
+        f32x16_t& d = p[t & 1];
+        if constexpr (kk == 0) d = f32x16_t{};
+        if constexpr (MODE == MODE_EXACT) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_codes(f.b[kk][j], u),
+                                                        widen_codes(f.a[kk][i], u), d, 0, 0, 0);
+        } else {
+          d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.b[kk][j], f.a[kk][i], d, 0, 0, 0, 0,
+                                                              0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        behind(q);
+        if constexpr (t > 0)
+          add_half(std::integral_constant<int, t - 1>{}, std::integral_constant<int, kk>{});
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      add_half(std::integral_constant<int, FM * FN - 1>{}, std::integral_constant<int, 0>{});
+      add_half(std::integral_constant<int, FM * FN - 1>{}, std::integral_constant<int, 1>{});
+    }
+  }
+
+  // The K loop with read-ahead.  Steps run in pairs (one per register set); a
+  // stage past the last holds zeros and adds nothing.
+  __device__ static __forceinline__ void loop_ring(f32x16_t (&acc)[FM][FN], uint32_t kt0,
+                                                   uint32_t nk, uint32_t K, uint32_t wm, uint32_t wn,
+                                                   bool sa_f32, bool sb_f32, const Src& c,
+                                                   const Lanes& ln) {
+    // stage 0 landed, the STAGES - 2 behind it in flight
+    wait_vm<(STAGES - 2) * LPS>();
+    barrier_lds();
+    const uint32_t part = (K & 15u) ? nk - 1 : 0xffffffffu;  // the stage to clear the tail of
+    if (kt0 == part) clear_tail(lds(), K & 127u);
+    Frags f[2];
+    {
+      const Ptrs p0 = ptrs(lds(), wm, wn);
+      load_scales(f[0], p0, wm, wn);
+      static_for<NL>([&](auto x) { load_frag<decltype(x)::value>(f[0], p0); });
+    }
+    uint32_t cur = 0;  // buffer of stage kt
+    auto step = [&](uint32_t kt, const Frags& now, Frags& then) {
+      // stage kt + 1 landed; every wave has read stage kt and is done with kt - 1
+      wait_vm<(STAGES - 3) * LPS>();
+      barrier_lds();
+      const uint32_t nb = cur + 1 == STAGES ? 0 : cur + 1;     // stage kt + 1
+      const uint32_t pb = cur == 0 ? STAGES - 1 : cur - 1;     // stage kt - 1, free
+      const Stage next = stage(c, ln, kt + STAGES - 1, pb);
+      dma_scales(c, ln, next, kt + STAGES - 1);
+      if (kt + 1 == part) clear_tail(lds() + nb * STAGE_BYTES, K & 127u);
+      const Ptrs np = ptrs(lds() + nb * STAGE_BYTES, wm, wn);
+      step_ring(acc, now, then, np, wm, wn, sa_f32, sb_f32, c, ln, next);
+      cur = nb;
+    };
+    for (uint32_t kt = kt0; kt < c.kt1; kt += 2) {
+      step(kt, f[0], f[1]);
+      step(kt + 1, f[1], f[0]);
+    }
+  }
+
   __device__ __attribute__((always_inline)) static void run(const BlockGemmArgs& a) {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t lane = threadIdx.x & 63u;
@@ -454,8 +596,11 @@ struct BlockGemm {
       dma_scales(c, ln, st, kt0 + s);
       static_for<ND>([&](auto x) { dma_one<decltype(x)::value>(c, ln, st); });
     }
+    if constexpr (RING) {
+      if (kt0 < kt1) loop_ring(acc, kt0, a.nk, a.K, wm, wn, sa_f32, sb_f32, c, ln);
+    }
     uint32_t buf = 0;
-    for (uint32_t kt = kt0; kt < kt1; ++kt) {
+    for (uint32_t kt = RING ? kt1 : kt0; kt < kt1; ++kt) {
       wait_vm<(STAGES - 2) * LPS>();
       barrier_lds();
       const uint32_t nb = buf == 0 ? STAGES - 1 : buf - 1;  // the buffer read in the last step
