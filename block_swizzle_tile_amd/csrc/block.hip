@@ -132,8 +132,9 @@ bst_status plan_workspace(Plan& p, int64_t rows, int64_t N) {
   return BST_OK;
 }
 
-// Tile and split of a product.  count: groups (0: plain).
-bst_status plan_gemm(int64_t count, int64_t M, int64_t N, int64_t K, const Sched& s, Plan& p) {
+// Tile and split of a product.  count: groups (0: plain); exact: an fp32 output.
+bst_status plan_gemm(int64_t count, int64_t M, int64_t N, int64_t K, bool exact, const Sched& s,
+                     Plan& p) {
   const int64_t cus = device_cu_count(), G = std::max<int64_t>(count, 1);
   const int64_t per = cdiv(M, G);  // rows of a group, on average
   auto tiles = [&](int64_t tm, int64_t tn) {
@@ -145,14 +146,15 @@ bst_status plan_gemm(int64_t count, int64_t M, int64_t N, int64_t K, const Sched
     p.tn = 128;
     if (per <= 32) p.tm = 32;
     else if (per <= 64) p.tm = 64;
-    else if (cdiv(M, 256) * cdiv(N, 256) * 4 >= cus * 3) p.tm = p.tn = 256;
+    else if (!exact && cdiv(M, 256) * cdiv(N, 256) * 4 >= cus * 3) p.tm = p.tn = 256;
     else if (cdiv(M, 128) * cdiv(N, 128) * 4 >= cus * 3) p.tm = 128;
     else p.tm = 64;
   }
   const bool known = (p.tn == 128 && (p.tm == 32 || p.tm == 64 || p.tm == 128)) ||
-                     (p.tm == 256 && p.tn == 256);
+                     (p.tm == 256 && p.tn == 256 && !exact);
   if (!known)
-    return set_error(BST_E_UNSUPPORTED, "no block-scaled kernel with tile %ux%u", p.tm, p.tn);
+    return set_error(BST_E_UNSUPPORTED, "no block-scaled kernel with tile %ux%u%s", p.tm, p.tn,
+                     exact ? " and an fp32 output" : "");
   p.tiles = tiles(p.tm, p.tn);
   const int64_t nk = cdiv(K, 128);
   int64_t split = s.split;
@@ -161,8 +163,10 @@ bst_status plan_gemm(int64_t count, int64_t M, int64_t N, int64_t K, const Sched
     split = 1;
   } else if (split == 0) {
     split = 1;
+    // one workgroup per CU: beyond that a split only adds partial sums (one row,
+    // 4096 x 4096: 10.3 us at half the CUs, 9.2 at all, 13.4 at twice)
     if (p.tiles > 0 && p.tiles < cus && nk >= 4)
-      split = std::max<int64_t>(1, std::min<int64_t>({cus * 2 / p.tiles, nk / 2, 16}));
+      split = std::max<int64_t>(1, std::min<int64_t>({cus / p.tiles, nk / 2, 16}));
   }
   if (nk == 0) split = 1;
   const int64_t ks = nk ? cdiv(nk, split) : 0;
@@ -266,7 +270,7 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
   const bool rows = !grouped && takes_rows(trans_b, M, s);
   Plan p;
   if (!rows) {
-    if ((st = plan_gemm(grouped ? G : 0, M, N, K, s, p)) != BST_OK) return st;
+    if ((st = plan_gemm(grouped ? G : 0, M, N, K, c == BST_F32, s, p)) != BST_OK) return st;
     if ((st = check_ws(p, ws, ws_bytes)) != BST_OK) return st;
   }
   const int mode = c == BST_F32 ? MODE_EXACT : sa == BST_E8M0 && sb == BST_E8M0 ? MODE_E8M0 : MODE_F32;
@@ -308,17 +312,19 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
   a.ckind = (uint32_t)c;
   a.cvec = vec_rows(C, ldc, 0, out_bytes(c));
   if (rows) {
-    const dim3 grid((uint32_t)cdiv(N, 16)), block(512);
-    const hipStream_t q = (hipStream_t)stream;
-    if (M <= 16 && mode == MODE_EXACT)
-      hipLaunchKernelGGL((block_rows_kernel<1, true>), grid, block, 0, q, a);
-    else if (M <= 16)
-      hipLaunchKernelGGL((block_rows_kernel<1, false>), grid, block, 0, q, a);
-    else if (mode == MODE_EXACT)
-      hipLaunchKernelGGL((block_rows_kernel<2, true>), grid, block, 0, q, a);
-    else
-      hipLaunchKernelGGL((block_rows_kernel<2, false>), grid, block, 0, q, a);
-    return launched(hipGetLastError(), "block-scaled product");
+    const int fn = cdiv(N, 32) >= 2 * device_cu_count() ? 2 : 1;
+    const dim3 grid((uint32_t)cdiv(N, 16 * fn)), block(512);
+    auto run = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, block, 0, (hipStream_t)stream, a);
+      return launched(hipGetLastError(), "block-scaled product");
+    };
+    const bool exact = mode == MODE_EXACT;
+    if (fn == 2) {
+      if (M <= 16) return exact ? run(block_rows_kernel<1, 2, true>) : run(block_rows_kernel<1, 2, false>);
+      return exact ? run(block_rows_kernel<2, 2, true>) : run(block_rows_kernel<2, 2, false>);
+    }
+    if (M <= 16) return exact ? run(block_rows_kernel<1, 1, true>) : run(block_rows_kernel<1, 1, false>);
+    return exact ? run(block_rows_kernel<2, 1, true>) : run(block_rows_kernel<2, 1, false>);
   }
   if (p.split > 1) {
     a.part = static_cast<float*>(ws);
@@ -433,10 +439,11 @@ bst_status quant_args(BlockQuantArgs& a, bst_dtype x, int64_t M, int64_t K, int3
   return BST_OK;
 }
 
-// Workgroups of the row kernels: 16 blocks per workgroup and step, as many
-// workgroups as stay resident (eight per CU), fewer when there is less.
+// Workgroups of the row kernels, 16 blocks each and step: enough that the last
+// ones to finish do not matter (16384 x 8192 bf16: 79 us with eight per CU, 74
+// with 64), fewer when there is less.
 uint32_t row_grid(uint32_t blocks) {
-  return (uint32_t)std::min<int64_t>(cdiv(blocks, 16), (int64_t)device_cu_count() * 8);
+  return (uint32_t)std::min<int64_t>(cdiv(blocks, 16), (int64_t)device_cu_count() * 64);
 }
 
 }  // namespace
@@ -469,11 +476,11 @@ bst_status bst_quant_block(bst_dtype x, int64_t M, int64_t K, int32_t block_rows
   } else {
     const uint32_t grid = row_grid(a.blocks);
     if (x == BST_F32)
-      hipLaunchKernelGGL((quant_rows_kernel<X_F32, 4>), dim3(grid), dim3(256), 0, s, a);
+      hipLaunchKernelGGL((quant_rows_kernel<X_F32>), dim3(grid), dim3(256), 0, s, a);
     else if (x == BST_BF16)
-      hipLaunchKernelGGL((quant_rows_kernel<X_BF16, 4>), dim3(grid), dim3(256), 0, s, a);
+      hipLaunchKernelGGL((quant_rows_kernel<X_BF16>), dim3(grid), dim3(256), 0, s, a);
     else
-      hipLaunchKernelGGL((quant_rows_kernel<X_F16, 4>), dim3(grid), dim3(256), 0, s, a);
+      hipLaunchKernelGGL((quant_rows_kernel<X_F16>), dim3(grid), dim3(256), 0, s, a);
   }
   return launched(hipGetLastError(), "quantisation");
 }
@@ -498,11 +505,11 @@ bst_status bst_dequant_block(bst_dtype x, int64_t M, int64_t K, int32_t block_ro
   const uint32_t grid = row_grid(a.blocks);
   const hipStream_t s = (hipStream_t)stream;
   if (x == BST_F32)
-    hipLaunchKernelGGL((dequant_kernel<X_F32, 4>), dim3(grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((dequant_kernel<X_F32>), dim3(grid), dim3(256), 0, s, a);
   else if (x == BST_BF16)
-    hipLaunchKernelGGL((dequant_kernel<X_BF16, 4>), dim3(grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((dequant_kernel<X_BF16>), dim3(grid), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((dequant_kernel<X_F16, 4>), dim3(grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((dequant_kernel<X_F16>), dim3(grid), dim3(256), 0, s, a);
   return launched(hipGetLastError(), "restoring");
 }
 
@@ -561,9 +568,13 @@ size_t bst_block_workspace_bytes(int kind, int64_t count, int64_t M, int64_t N, 
     return 0;
   }
   if (kind == 3 && takes_rows(1, M, s)) return 0;
-  const bst_status st = kind == 0 || kind == 3 ? plan_gemm(0, M, N, K, s, p)
-                                               : plan_grad(kind == 2 ? count : 0, M, N, K, s, p);
-  return st == BST_OK ? p.ws : 0;
+  if (kind == 1 || kind == 2)
+    return plan_grad(kind == 2 ? count : 0, M, N, K, s, p) == BST_OK ? p.ws : 0;
+  // the output type, which may change the tile, is not known here: enough for any
+  Plan q;
+  const bst_status other = plan_gemm(0, M, N, K, true, s, q);
+  const bst_status st = plan_gemm(0, M, N, K, false, s, p);
+  return std::max(st == BST_OK ? p.ws : 0, other == BST_OK ? q.ws : 0);
 }
 
 }  // extern "C"

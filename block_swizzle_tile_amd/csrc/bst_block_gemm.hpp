@@ -495,6 +495,33 @@ struct BlockGemm {
     }
   }
 
+  // The K loop of a wave none of whose rows or columns is inside the matrix: it
+  // loads its share, passes the same barriers as the others, and leaves the
+  // matrix unit to the waves beside it (a group's last tile is seldom full).
+  __device__ static __forceinline__ void loop_idle(uint32_t kt0, uint32_t nk, uint32_t K,
+                                                   const Src& c, const Lanes& ln) {
+    const uint32_t part = (K & 15u) ? nk - 1 : 0xffffffffu;
+    uint32_t cur = 0;
+    if constexpr (RING) {
+      if (kt0 >= c.kt1) return;
+      wait_vm<(STAGES - 2) * LPS>();
+      barrier_lds();
+      if (kt0 == part) clear_tail(lds(), K & 127u);
+    }
+    const uint32_t end = RING ? kt0 + (c.kt1 - kt0 + 1) / 2 * 2 : c.kt1;
+    for (uint32_t kt = kt0; kt < end; ++kt) {
+      wait_vm<(STAGES - (RING ? 3 : 2)) * LPS>();
+      barrier_lds();
+      const uint32_t nb = cur + 1 == STAGES ? 0 : cur + 1;
+      const Stage next = stage(c, ln, kt + STAGES - 1, cur == 0 ? STAGES - 1 : cur - 1);
+      dma_scales(c, ln, next, kt + STAGES - 1);
+      static_for<ND>([&](auto x) { dma_one<decltype(x)::value>(c, ln, next); });
+      if (RING && kt + 1 == part) clear_tail(lds() + nb * STAGE_BYTES, K & 127u);
+      if (!RING && kt == part) clear_tail(lds() + cur * STAGE_BYTES, K & 127u);
+      cur = nb;
+    }
+  }
+
   __device__ __attribute__((always_inline)) static void run(const BlockGemmArgs& a) {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t lane = threadIdx.x & 63u;
@@ -596,20 +623,23 @@ struct BlockGemm {
       dma_scales(c, ln, st, kt0 + s);
       static_for<ND>([&](auto x) { dma_one<decltype(x)::value>(c, ln, st); });
     }
-    if constexpr (RING) {
+    if (wm * TM >= rows_left || wn * TN >= cols_left) {
+      loop_idle(kt0, a.nk, a.K, c, ln);
+    } else if constexpr (RING) {
       if (kt0 < kt1) loop_ring(acc, kt0, a.nk, a.K, wm, wn, sa_f32, sb_f32, c, ln);
-    }
-    uint32_t buf = 0;
-    for (uint32_t kt = RING ? kt1 : kt0; kt < kt1; ++kt) {
-      wait_vm<(STAGES - 2) * LPS>();
-      barrier_lds();
-      const uint32_t nb = buf == 0 ? STAGES - 1 : buf - 1;  // the buffer read in the last step
-      const Stage next = stage(c, ln, kt + STAGES - 1, nb);
-      dma_scales(c, ln, next, kt + STAGES - 1);
-      lds_t* base = lds() + buf * STAGE_BYTES;
-      if (kt + 1 == a.nk && (a.K & 15u)) clear_tail(base, a.K & 127u);
-      compute(acc, base, wm, wn, sa_f32, sb_f32, c, ln, next);
-      buf = buf + 1 == STAGES ? 0 : buf + 1;
+    } else {
+      uint32_t buf = 0;
+      for (uint32_t kt = kt0; kt < kt1; ++kt) {
+        wait_vm<(STAGES - 2) * LPS>();
+        barrier_lds();
+        const uint32_t nb = buf == 0 ? STAGES - 1 : buf - 1;  // the buffer read in the last step
+        const Stage next = stage(c, ln, kt + STAGES - 1, nb);
+        dma_scales(c, ln, next, kt + STAGES - 1);
+        lds_t* base = lds() + buf * STAGE_BYTES;
+        if (kt + 1 == a.nk && (a.K & 15u)) clear_tail(base, a.K & 127u);
+        compute(acc, base, wm, wn, sa_f32, sb_f32, c, ln, next);
+        buf = buf + 1 == STAGES ? 0 : buf + 1;
+      }
     }
     // ---- every wave is done with the stages: their LDS holds the strips
     __builtin_amdgcn_s_waitcnt(0);

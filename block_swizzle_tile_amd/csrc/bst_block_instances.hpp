@@ -63,7 +63,8 @@ hipError_t launch_block_grad(uint32_t grid, hipStream_t st, const BlockGradArgs&
       BST_BLOCK_GEMM(BM, BN, WM, WN, ST, TB, MODE_EXACT, GR)
 #define BST_BLOCK_GEMM_TILES(TB, GR)                                                          \
   BST_BLOCK_GEMM_TILE(32, 128, 1, 4, 4, TB, GR), BST_BLOCK_GEMM_TILE(64, 128, 2, 4, 4, TB, GR), \
-      BST_BLOCK_GEMM_TILE(128, 128, 2, 4, 4, TB, GR), BST_BLOCK_GEMM_TILE(256, 256, 2, 4, 2, TB, GR)
+      BST_BLOCK_GEMM_TILE(128, 128, 2, 4, 4, TB, GR), \
+      BST_BLOCK_GEMM(256, 256, 2, 4, 2, TB, MODE_E8M0, GR), BST_BLOCK_GEMM(256, 256, 2, 4, 2, TB, MODE_F32, GR)
 
 #define BST_BLOCK_GRAD(BK, BN, WM, WN, DY) \
   BlockGradInstance { BK, BN, DY, BlockGrad<BK, BN, WM, WN, DY>::D, &launch_block_grad<BK, BN, WM, WN, DY> }

@@ -100,41 +100,27 @@ __device__ __forceinline__ void put_codes(uint8_t* q, const u32x2_t& o, uint32_t
     if ((uint32_t)e < live) q[e] = (uint8_t)(o[e / 4] >> (8 * (e & 3)));
 }
 
-// Blocks of 1 x 128: 16 blocks per workgroup and step, U steps in flight.
-template <int XK, int U>
+// Blocks of 1 x 128: 16 blocks per workgroup and step, one step in flight per
+// thread.  More steps in flight were slower (16384 x 8192 bf16: 79 us at one,
+// 80 at two, 95 at four): the eight waves per SIMD that fit hide the latency,
+// and their loads stay near each other in memory.
+template <int XK>
 __global__ void __launch_bounds__(256) quant_rows_kernel(BlockQuantArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int ES = XK == X_F32 ? 4 : 2;
   const uint32_t sub = threadIdx.x & 15u, step = gridDim.x * 16u;
-  // step <= 2^20 and blocks < 2^31: the sums below stay in 32 bits
-  for (uint32_t b0 = blockIdx.x * 16u + (threadIdx.x >> 4); b0 < a.blocks; b0 += U * step) {
-    float v[U][8];
-    uint32_t live[U], row[U], kb[U];
+  // step < 2^20 and blocks < 2^31: b stays in 32 bits
+  for (uint32_t b = blockIdx.x * 16u + (threadIdx.x >> 4); b < a.blocks; b += step) {
+    const uint32_t row = a.by_kb.div(b), kb = b - row * a.kb;
+    const uint32_t k = kb * 128u + sub * 8u;
+    float v[8] = {};
+    if (k < a.K) load8<XK>(v, a.X + ((int64_t)row * a.ldx + k) * ES, a.K - k, a.xvec != 0);
+    uint32_t top = top8(v);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t b = b0 + u * step;
-      row[u] = a.by_kb.div(b);
-      kb[u] = b - row[u] * a.kb;
-      const uint32_t k = kb[u] * 128u + sub * 8u;
-      live[u] = b < a.blocks && k < a.K ? a.K - k : 0u;
-      if (live[u])
-        load8<XK>(v[u], a.X + ((int64_t)row[u] * a.ldx + k) * ES, live[u], a.xvec != 0);
-      else
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (b0 + u * step >= a.blocks) break;  // the same in a block's 16 lanes
-      uint32_t top = top8(v[u]);
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 16));
-      const uint32_t e = scale_byte(top);
-      const uint32_t k = kb[u] * 128u + sub * 8u;
-      if (live[u])
-        put_codes(a.Q + (int64_t)row[u] * a.ldq + k, codes8(v[u], e), live[u], a.qvec != 0);
-      if (sub == 0) a.S[(int64_t)row[u] * a.lds + kb[u]] = (uint8_t)e;
-    }
+    for (int d = 1; d < 16; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 16));
+    const uint32_t e = scale_byte(top);
+    if (k < a.K) put_codes(a.Q + (int64_t)row * a.ldq + k, codes8(v, e), a.K - k, a.qvec != 0);
+    if (sub == 0) a.S[(int64_t)row * a.lds + kb] = (uint8_t)e;
   }
 #endif
 }
@@ -177,62 +163,47 @@ __global__ void __launch_bounds__(256) quant_square_kernel(BlockQuantArgs a) {
 }
 
 // Codes back to values: 16 blocks of 1 x 128 per workgroup and step.
-template <int XK, int U>
+template <int XK>
 __global__ void __launch_bounds__(256) dequant_kernel(BlockQuantArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int ES = XK == X_F32 ? 4 : 2;
   constexpr float LARGEST = XK == X_F32 ? 3.4028234663852886e38f
                             : XK == X_BF16 ? 3.3895313892515355e38f : 65504.0f;
   const uint32_t sub = threadIdx.x & 15u, step = gridDim.x * 16u;
-  for (uint32_t b0 = blockIdx.x * 16u + (threadIdx.x >> 4); b0 < a.blocks; b0 += U * step) {
-    u32x2_t q[U];
-    float f[U];
-    uint32_t live[U], row[U], k[U];
+  for (uint32_t b = blockIdx.x * 16u + (threadIdx.x >> 4); b < a.blocks; b += step) {
+    const uint32_t row = a.by_kb.div(b), kb = b - row * a.kb;
+    const uint32_t k = kb * 128u + sub * 8u;
+    if (k >= a.K) continue;
+    const uint32_t live = a.K - k;
+    const uint8_t* p = a.Q + (int64_t)row * a.ldq + k;
+    u32x2_t q = {0u, 0u};
+    if (a.qvec && live >= 8u) {
+      q = *(const u32x2_t*)p;
+    } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t b = b0 + u * step;
-      row[u] = a.by_kb.div(b);
-      const uint32_t kb = b - row[u] * a.kb;
-      k[u] = kb * 128u + sub * 8u;
-      live[u] = b < a.blocks && k[u] < a.K ? a.K - k[u] : 0u;
-      q[u] = u32x2_t{0u, 0u};
-      f[u] = 0.0f;
-      if (live[u]) {
-        const uint8_t* p = a.Q + (int64_t)row[u] * a.ldq + k[u];
-        if (a.qvec && live[u] >= 8u) {
-          q[u] = *(const u32x2_t*)p;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if ((uint32_t)e < live[u]) q[u][e / 4] |= (uint32_t)p[e] << (8 * (e & 3));
-        }
-        const int64_t at = (int64_t)(a.block_rows == 1 ? row[u] : row[u] / 128u) * a.lds + kb;
-        f[u] = a.s_f32 ? ((const float*)a.S)[at] : e8m0_value(a.S[at]);
-      }
+      for (int e = 0; e < 8; ++e)
+        if ((uint32_t)e < live) q[e / 4] |= (uint32_t)p[e] << (8 * (e & 3));
     }
+    const int64_t at = (int64_t)(a.block_rows == 1 ? row : row / 128u) * a.lds + kb;
+    const float f = a.s_f32 ? ((const float*)a.S)[at] : e8m0_value(a.S[at]);
+    const bool finite = __builtin_fabsf(f) < __builtin_inff();
+    float v[8];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!live[u]) continue;
-      float v[8];
-      const bool sat = __builtin_fabsf(f[u]) < __builtin_inff();  // a finite scale
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        typedef float f2 __attribute__((ext_vector_type(2)));
-        const uint32_t w = q[u][d / 2];
-        const f2 c = (d & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true)
-                             : __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
-        v[2 * d] = c[0] * f[u];
-        v[2 * d + 1] = c[1] * f[u];
-      }
-      // a finite code never becomes infinite (NaN passes: it fails both comparisons)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (sat && v[e] > LARGEST) v[e] = LARGEST;
-        if (sat && v[e] < -LARGEST) v[e] = -LARGEST;
-      }
-      uint8_t* p = a.Xo + ((int64_t)row[u] * a.ldx + k[u]) * ES;
-      put_run<8>(p, nullptr, v, live[u], a.xvec != 0 && live[u] >= 8u, XK);
+    for (int d = 0; d < 4; ++d) {
+      typedef float f2 __attribute__((ext_vector_type(2)));
+      const f2 c = (d & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)q[d / 2], true)
+                           : __builtin_amdgcn_cvt_pk_f32_fp8((int)q[d / 2], false);
+      v[2 * d] = c[0] * f;
+      v[2 * d + 1] = c[1] * f;
     }
+    // a finite code never becomes infinite (NaN passes: it fails both comparisons)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (finite && v[e] > LARGEST) v[e] = LARGEST;
+      if (finite && v[e] < -LARGEST) v[e] = -LARGEST;
+    }
+    put_run<8>(a.Xo + ((int64_t)row * a.ldx + k) * ES, nullptr, v, live, a.xvec != 0 && live >= 8u,
+               XK);
   }
 #endif
 }

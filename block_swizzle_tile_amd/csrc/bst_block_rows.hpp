@@ -17,9 +17,9 @@ namespace bst {
 
 typedef float f32x4v_t __attribute__((ext_vector_type(4)));
 
-template <int FM, bool EXACT>
+template <int FM, int FN, bool EXACT>
 struct BlockRows {
-  static constexpr int NW = 8, NT = 64 * NW, UNROLL = 4;
+  static constexpr int NW = 8, NT = 64 * NW, UNROLL = FM * FN == 4 ? 2 : 4;
 
   // 16 codes at p, of which `left` are inside K; the rest may be anything
   // (inside the row's pitch) and become zeros.
@@ -57,13 +57,19 @@ struct BlockRows {
   }
 
   __device__ __attribute__((always_inline)) static void run(const BlockGemmArgs& a) {
-    __shared__ f32x4v_t sums[FM][NW][64];
+    __shared__ f32x4v_t sums[FM * FN][NW][64];
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u;
     const uint32_t r = lane & 15u, q = lane >> 4;  // operand row; K 32q .. 32q+31 of a block
-    const uint32_t n0 = blockIdx.x * 16u, n = n0 + r;
-    const bool live_n = n < a.N;
-    const uint8_t* b = a.B + (int64_t)(live_n ? n : 0) * a.ldb + 32 * q;
-    const int64_t sb = (int64_t)(n0 / kScaleBlock) * a.ldsb;  // one block: 16 divides 128
+    const uint32_t n0 = blockIdx.x * (16u * FN);
+    const uint8_t* b[FN];
+    bool live_n[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const uint32_t n = n0 + j * 16 + r;
+      live_n[j] = n < a.N;
+      b[j] = a.B + (int64_t)(live_n[j] ? n : 0) * a.ldb + 32 * q;
+    }
+    const int64_t sb = (int64_t)(n0 / kScaleBlock) * a.ldsb;  // one block: 32 divides 128
     const uint8_t* ap[FM];
     int64_t sap[FM];
     bool live_m[FM];
@@ -74,18 +80,21 @@ struct BlockRows {
       ap[i] = a.A + (int64_t)(live_m[i] ? m : 0) * a.lda + 32 * q;
       sap[i] = (int64_t)(live_m[i] ? m : 0) * a.ldsa;
     }
-    f32x4v_t acc[FM];
+    f32x4v_t acc[FM][FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) acc[i] = f32x4v_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4v_t{0.0f, 0.0f, 0.0f, 0.0f};
     for (uint32_t k0 = wave * UNROLL; k0 < a.nk; k0 += NW * UNROLL) {
-      i32x8_t bv[UNROLL], av[UNROLL][FM];
+      i32x8_t bv[UNROLL][FN], av[UNROLL][FM];
       float f[UNROLL][FM];
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u) {
         const uint32_t kb = k0 + u;
         const int64_t at = (int64_t)kb * 128;
         const int left = kb < a.nk ? (int)(a.K - kb * 128u) - 32 * (int)q : 0;
-        bv[u] = codes32(b + at, live_n ? left : 0);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) bv[u][j] = codes32(b[j] + at, live_n[j] ? left : 0);
         const float fb = kb < a.nk ? scale(a.sb, sb + kb, a.sb_f32 != 0) : 0.0f;
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
@@ -96,21 +105,26 @@ struct BlockRows {
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          const f32x4v_t p = product(bv[u], av[u][i]);
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(f[u][i], p[e], acc[i][e]);
-        }
+          for (int j = 0; j < FN; ++j) {
+            const f32x4v_t p = product(bv[u][j], av[u][i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(f[u][i], p[e], acc[i][j][e]);
+          }
     }
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sums[i][wave][lane] = acc[i];
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sums[i * FN + j][wave][lane] = acc[i][j];
     __syncthreads();
-    // lane l of wave i: row 16 i + (l & 15) of C, columns n0 + 4 (l >> 4) + 0..3
-    if (wave >= (uint32_t)FM) return;
+    // wave w ends fragment (w / FN, w % FN); lane l: row l & 15 of it, columns
+    // 4 (l >> 4) + 0..3
+    if (wave >= (uint32_t)(FM * FN)) return;
     f32x4v_t s = sums[wave][0][lane];
 #pragma unroll
     for (int w = 1; w < NW; ++w) s += sums[wave][w][lane];
-    const uint32_t m = wave * 16 + r, c = n0 + 4 * q;
+    const uint32_t m = wave / FN * 16 + r, c = n0 + wave % FN * 16 + 4 * q;
     if (m >= a.M || c >= a.N) return;
     const int64_t es = a.ckind == OUT_F32 ? 4 : 2;
     float v[4] = {s[0], s[1], s[2], s[3]};
@@ -119,10 +133,10 @@ struct BlockRows {
   }
 };
 
-template <int FM, bool EXACT>
+template <int FM, int FN, bool EXACT>
 __global__ void __launch_bounds__(512) block_rows_kernel(BlockGemmArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  BlockRows<FM, EXACT>::run(a);
+  BlockRows<FM, FN, EXACT>::run(a);
 #endif
 }
 

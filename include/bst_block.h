@@ -87,7 +87,7 @@ bst_status bst_dequant_block(bst_dtype x, int64_t M, int64_t K, int32_t block_ro
  *   Up to 32 rows of A with trans_b = 1 and no tile or split asked for run on
  *   a kernel of their own, which reads every weight once in one launch.
  *   sched: NULL, or a schedule of which tile_m x tile_n (0 x 0 = chosen by
- *   the sizes; 32x128, 64x128, 128x128, 256x256), swizzle_offset,
+ *   the sizes; 32x128, 64x128, 128x128, and 256x256 for 16-bit outputs), swizzle_offset,
  *   swizzle_direction, xcd_remap and split_k (0 = chosen, at most 64) are used; tile_k
  *   is 0 or 128 and grid, path, shuffle_k, dynamic and preload are 0
  *   (BST_E_UNSUPPORTED otherwise).

@@ -121,6 +121,7 @@ def test_gemm_refusals(L):
     assert gemm(L, ldsa=8 << 20) == _lib.E_UNSUPPORTED
     assert gemm(L, ldc=255) == _lib.E_INVAL
     assert gemm(L, sched=S(tile=(96, 96))) == _lib.E_UNSUPPORTED
+    assert gemm(L, c=FF, sched=S(tile=(256, 256))) == _lib.E_UNSUPPORTED    # 16-bit outputs only
     assert gemm(L, sched=S(offset=0)) == _lib.E_INVAL
     assert gemm(L, sched=S(direction=3)) == _lib.E_INVAL
     assert gemm(L, sched=S(split_k=65)) == _lib.E_INVAL
