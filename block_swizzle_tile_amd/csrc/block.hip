@@ -198,10 +198,19 @@ bst_status plan_grad(int64_t count, int64_t M, int64_t N, int64_t K, const Sched
   return plan_workspace(p, G * K, N);
 }
 
-// Products that the kernel for a few rows takes: weights stored N x K, and
-// neither a tile nor a split asked for.
-bool takes_rows(int32_t trans_b, int64_t M, const Sched& s) {
-  return trans_b && M <= 32 && s.tm == 0 && s.tn == 0 && s.split == 0;
+// Products that the kernels for a few rows take, if no tile and no split is
+// asked for.  They need one launch and no partial sums, but a workgroup walks
+// all of K, so they lose to a split where K is long or the rows fill more
+// operands.  Weights N x K: 16 rows 7.1 us against 10.3 (4096 x 4096), 18.5
+// against 16.2 at K = 14336; 32 rows 9.9 against 10.3 and 27.7 against 17.
+// Weights K x N: one row 7.1 us against 9.2 (4096 x 4096), 31 against 15 at K =
+// 14336; 33 rows 9.2 against 10.6 at K = 2056 and 12.0 against 11.7 at 4096;
+// and past 16384 columns the tiles fill the chip unsplit (16.5 against 14.8).
+bool takes_rows(int32_t trans_b, int64_t M, int64_t N, int64_t K, const Sched& s) {
+  if (s.tm != 0 || s.tn != 0 || s.split != 0) return false;
+  const int64_t nk = cdiv(K, 128);
+  if (trans_b) return M <= 16 || (M <= 32 && nk <= 32);
+  return M <= 64 && cdiv(nk, 8) * cdiv(M, 32) <= 6 && cdiv(N, 128) * 2 < device_cu_count();
 }
 
 bst_status check_ws(const Plan& p, const void* ws, size_t bytes) {
@@ -267,7 +276,7 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
     if (grouped && strideB % 16 != 0)
       return set_error(BST_E_ALIGN, "strideB must be a multiple of 16 bytes");
   }
-  const bool rows = !grouped && takes_rows(trans_b, M, s);
+  const bool rows = !grouped && takes_rows(trans_b, M, N, K, s);
   Plan p;
   if (!rows) {
     if ((st = plan_gemm(grouped ? G : 0, M, N, K, c == BST_F32, s, p)) != BST_OK) return st;
@@ -313,12 +322,17 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
   a.cvec = vec_rows(C, ldc, 0, out_bytes(c));
   if (rows) {
     const int fn = cdiv(N, 32) >= 2 * device_cu_count() ? 2 : 1;
-    const dim3 grid((uint32_t)cdiv(N, 16 * fn)), block(512);
+    a.grid = (uint32_t)cdiv(N, trans_b ? 16 * fn : 64);
+    const dim3 grid(a.grid), block(512);
     auto run = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, block, 0, (hipStream_t)stream, a);
       return launched(hipGetLastError(), "block-scaled product");
     };
     const bool exact = mode == MODE_EXACT;
+    if (!trans_b) {
+      if (M <= 32) return exact ? run(block_rows_n_kernel<1, true>) : run(block_rows_n_kernel<1, false>);
+      return exact ? run(block_rows_n_kernel<2, true>) : run(block_rows_n_kernel<2, false>);
+    }
     if (fn == 2) {
       if (M <= 16) return exact ? run(block_rows_kernel<1, 2, true>) : run(block_rows_kernel<1, 2, false>);
       return exact ? run(block_rows_kernel<2, 2, true>) : run(block_rows_kernel<2, 2, false>);
@@ -567,7 +581,7 @@ size_t bst_block_workspace_bytes(int kind, int64_t count, int64_t M, int64_t N, 
     set_error(BST_E_INVAL, "group count %lld outside [1, %d]", (long long)count, kMaxGroups);
     return 0;
   }
-  if (kind == 3 && takes_rows(1, M, s)) return 0;
+  if ((kind == 0 || kind == 3) && takes_rows(kind == 3, M, N, K, s)) return 0;
   if (kind == 1 || kind == 2)
     return plan_grad(kind == 2 ? count : 0, M, N, K, s, p) == BST_OK ? p.ws : 0;
   // the output type, which may change the tile, is not known here: enough for any

@@ -84,15 +84,16 @@ bst_status bst_dequant_block(bst_dtype x, int64_t M, int64_t K, int32_t block_ro
  *   exponent and drop what is below 2^-13 of that (about 1.5e-5 of a result);
  *   an fp32 output is computed on bf16 instructions from the same codes,
  *   which keep fp32 throughout, and takes up to twice as long.
- *   Up to 32 rows of A with trans_b = 1 and no tile or split asked for run on
- *   a kernel of their own, which reads every weight once in one launch.
+ *   A few rows of A (at most 32, or 64 with trans_b = 0) run on kernels of
+ *   their own where K is not too long and no tile or split is asked for; they
+ *   read every weight once, in one launch and without a workspace.
  *   sched: NULL, or a schedule of which tile_m x tile_n (0 x 0 = chosen by
  *   the sizes; 32x128, 64x128, 128x128, and 256x256 for 16-bit outputs), swizzle_offset,
  *   swizzle_direction, xcd_remap and split_k (0 = chosen, at most 64) are used; tile_k
  *   is 0 or 128 and grid, path, shuffle_k, dynamic and preload are 0
  *   (BST_E_UNSUPPORTED otherwise).
- *   ws: bst_block_workspace_bytes(0 or 3, ...) bytes, 16-byte aligned (may
- *   be NULL when that is 0).
+ *   ws: bst_block_workspace_bytes(0, or 3 with trans_b = 1, ...) bytes,
+ *   16-byte aligned (may be NULL when that is 0).
  *   BST_E_UNSUPPORTED if 256 rows of A or B (with trans_b = 0: 128 rows of
  *   B) span 2 GiB.
  */
@@ -160,10 +161,10 @@ bst_status bst_grouped_weight_grad(bst_dtype dy, bst_dtype dw, int32_t G,
 
 /*
  * bst_block_workspace_bytes -- workspace bytes of a call with these sizes on
- * the current device: kind 0 bst_gemm_block_scaled (3: with trans_b = 1,
- * where a few rows never need one; what 0 says is always enough), 1
- * bst_weight_grad, 2 bst_grouped_weight_grad (count = G, M = total_m).  0
- * where no split runs, and for invalid arguments (with the last error set).
+ * the current device: kind 0 bst_gemm_block_scaled with trans_b = 0, 3 with
+ * trans_b = 1, 1 bst_weight_grad, 2 bst_grouped_weight_grad (count = G, M =
+ * total_m).  0 where no split runs, and for invalid arguments (with the last
+ * error set).
  */
 size_t bst_block_workspace_bytes(int kind, int64_t count, int64_t M, int64_t N, int64_t K,
                                  const bst_sched* sched);

@@ -146,8 +146,9 @@ def test_workspace(L):
     assert L.bst_block_workspace_bytes(4, 1, 1, 1, 1, None) == 0
     assert b"kind" in L.bst_last_error()
     assert L.bst_block_workspace_bytes(2, 0, 1, 1, 1, None) == 0
-    assert L.bst_block_workspace_bytes(0, 1, 1, 512, 4096, None) > 0
-    assert L.bst_block_workspace_bytes(3, 1, 1, 512, 4096, None) == 0    # few rows, weights N x K
+    assert L.bst_block_workspace_bytes(0, 1, 1, 512, 16384, None) > 0
+    assert L.bst_block_workspace_bytes(3, 1, 1, 512, 16384, None) == 0    # few rows: one launch
+    assert L.bst_block_workspace_bytes(0, 1, 1, 512, 2048, None) == 0
     # a split never has an empty slice: 3 blocks of K cut 8 ways are 3 slices
     s = bst.make_sched(tile=(64, 128), split_k=8)
     assert L.bst_block_workspace_bytes(0, 1, 64, 256, 384, ctypes.byref(s)) == 3 * 64 * 256 * 4

@@ -279,7 +279,7 @@ def test_product(kinds, tb):
 def test_product_default_schedule(M):
     """Few rows (single tokens) over longer K, where the split is chosen by the sizes."""
     for tb in (False, True):
-        for N, K in [(512, 4096), (1040, 1552), (4096, 512)]:
+        for N, K in [(512, 4096), (1040, 1552), (4096, 512), (200, 9000)]:
             A, sa, B, sb = operands(M, N, K, tb, ("e8m0", "f32"), gen(M), extra=0)
             ref, den = ref_product(A, sa, B, sb, tb)
             say("default", M, N, K, tb)
@@ -540,10 +540,10 @@ def test_experts_step():
 def test_streams_and_graphs():
     """Calls on two streams at once, each with a split (a workspace each), then a captured step
     replayed with new inputs between eager calls: every result has the eager call's bits."""
-    M, N, K = 24, 256, 2048
+    M, N, K = 40, 256, 8192
     sets = [operands(M, N, K, tb, ("e8m0", "f32"), gen(20 + tb)) for tb in (False, True)]
     want = [bst.gemm_block_scaled(A, B, sa, sb, trans_b=bool(i)) for i, (A, sa, B, sb) in enumerate(sets)]
-    assert bst.block_workspace_bytes(0, 1, M, N, K) > 0
+    assert bst.block_workspace_bytes(0, 1, M, N, K) > 0 and bst.block_workspace_bytes(3, 1, M, N, K) > 0
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
     got = [None, None]
