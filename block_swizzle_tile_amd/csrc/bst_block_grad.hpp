@@ -11,8 +11,8 @@
 // sums.  Both operands lie in LDS row by row (m); the transposing reads turn
 // 8 rows of a column into an operand of the 32x32x16 bf16 instruction.
 //
-// Global loads of stage s+1 are in registers while stage s is multiplied, and
-// are converted and written to the other LDS buffer behind it.
+// A stage's global loads are issued a whole step before they are converted and
+// written to LDS, at the top of the step before the one that multiplies them.
 #pragma once
 
 #include "bst_block.hpp"
@@ -67,9 +67,6 @@ struct BlockGrad {
   static constexpr int XCH = BK / 16, YCH = BN / 8;  // loads per row: 16 codes, 8 gradients
   static constexpr int XL = D * XCH / NT, YL = D * YCH / NT;  // loads per thread
   static constexpr int KSTEPS = D / 16;
-  // stages held in registers ahead of LDS: the 128 x 128 tile computes a stage
-  // in less than a load's latency and has the registers for two
-  static constexpr int AHEAD = BK == 128 ? 2 : 1;
 
   static_assert(D * XCH % NT == 0 && D * YCH % NT == 0, "whole loads");
   static_assert(2 * STAGE_BYTES + (int)sizeof(RowGroups) <= 160 * 1024, "LDS budget");
@@ -274,24 +271,20 @@ struct BlockGrad {
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
     if (cnt > 0) {
-      // stage i is in h[i % AHEAD] until it is written to buffer i % 2, one
-      // step before it is multiplied; loads past the last row read nothing
-      Held h[AHEAD];
-      static_for<AHEAD>([&](auto i) { load(h[decltype(i)::value], c, decltype(i)::value * D); });
-      store(h[0], lds());
-      load(h[0], c, AHEAD * D);
-      auto step = [&](uint32_t r, auto parity) {  // the stage at row r, in buffer `parity`
-        constexpr int B = decltype(parity)::value, H = (B + 1) % AHEAD;
-        __syncthreads();  // its buffer is written, and the other one read
-        compute(acc, lds() + B * STAGE_BYTES, wm, wn);
+      Held h;
+      load(h, c, 0);
+      store(h, lds());
+      load(h, c, D);
+      uint32_t buf = 0;
+      for (uint32_t r = 0; r < cnt; r += D) {
+        __syncthreads();  // buffer buf is written, and the other one read
+        // loads past the last row read nothing
         if (r + D < cnt) {
-          store(h[H], lds() + (B ^ 1) * STAGE_BYTES);
-          load(h[H], c, r + (1 + AHEAD) * D);
+          store(h, lds() + (buf ^ 1u) * STAGE_BYTES);
+          load(h, c, r + 2 * D);
         }
-      };
-      for (uint32_t r = 0; r < cnt; r += 2 * D) {
-        step(r, std::integral_constant<int, 0>{});
-        if (r + D < cnt) step(r + D, std::integral_constant<int, 1>{});
+        compute(acc, lds() + buf * STAGE_BYTES, wm, wn);
+        buf ^= 1u;
       }
       __syncthreads();
     }
