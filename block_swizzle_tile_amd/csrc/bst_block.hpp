@@ -24,11 +24,15 @@ __device__ __forceinline__ float e8m0_value(uint32_t e) {
   return __builtin_bit_cast(float, bits);
 }
 
-// Groups of stacked rows, in LDS: each group's first task and first row, and
-// the totals behind the last.
+// Groups of stacked rows, in LDS: each group's first row, its first task among
+// the full tile-rows, and its first tile-row among the partial ones (a group
+// has at most one), with the totals behind the last group.  The partial tiles
+// come after all full ones: they are the shorter tasks, and workgroups start
+// in order, so the chip's last round is filled with them.
 struct RowGroups {
-  uint32_t first_task[kMaxGroups + 1];
   uint32_t first_row[kMaxGroups + 1];
+  uint32_t first_task[kMaxGroups + 1];
+  uint32_t first_tail[kMaxGroups + 1];
 };
 
 // Built by wave 0 with a scan over the groups (lane l holds groups l*per ..):
@@ -47,26 +51,47 @@ __device__ inline void build_row_groups(RowGroups& t, const int32_t* group_m, ui
       if ((int)lane >= d) sum += o;
     }
     int64_t at = sum - rows;  // rows before this lane's groups, not yet cut
-    uint32_t tasks = 0;
+    uint32_t tasks = 0, tails = 0;
     for (uint32_t g = g0; g < g1; ++g) {
       const uint32_t lo = at < (int64_t)total_m ? (uint32_t)at : total_m;
       at += group_m[g] > 0 ? group_m[g] : 0;
       const uint32_t hi = at < (int64_t)total_m ? (uint32_t)at : total_m;
       t.first_row[g] = lo;
       t.first_task[g] = tasks;
-      tasks += (hi - lo + bm - 1) / bm * loops_n;
+      t.first_tail[g] = tails;
+      tasks += (hi - lo) / bm * loops_n;
+      tails += (hi - lo) % bm != 0 ? 1u : 0u;
       if (g + 1 == G) t.first_row[G] = hi;
     }
-    uint32_t ts = tasks;
+    uint32_t ts = tasks, ls = tails;
     for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t o = (uint32_t)__shfl_up((int)ts, d);
-      if ((int)lane >= d) ts += o;
+      const uint32_t o = (uint32_t)__shfl_up((int)ts, d), l = (uint32_t)__shfl_up((int)ls, d);
+      if ((int)lane >= d) {
+        ts += o;
+        ls += l;
+      }
     }
-    const uint32_t base = ts - tasks;
-    for (uint32_t g = g0; g < g1; ++g) t.first_task[g] += base;
-    if (lane == 63u) t.first_task[G] = ts;
+    for (uint32_t g = g0; g < g1; ++g) {
+      t.first_task[g] += ts - tasks;
+      t.first_tail[g] += ls - tails;
+    }
+    if (lane == 63u) {
+      t.first_task[G] = ts;
+      t.first_tail[G] = ls;
+    }
   }
   __syncthreads();
+}
+
+// The last group whose first entry is at most x (groups without entries of
+// their own share the next one's).
+__device__ __forceinline__ uint32_t find_group(const uint32_t* first, uint32_t G, uint32_t x) {
+  uint32_t lo = 0, hi = G - 1;
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // ------------------------------------------------------------ output ------

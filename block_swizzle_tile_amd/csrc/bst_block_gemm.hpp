@@ -533,19 +533,24 @@ struct BlockGemm {
       __shared__ RowGroups groups;
       const uint32_t loops_n = (a.N + BN - 1) / BN;
       build_row_groups(groups, a.group_m, a.G, a.M, BM, loops_n);
-      const uint32_t T = groups.first_task[a.G];
-      if (blockIdx.x >= T) return;  // the whole workgroup
-      const uint32_t u = logical_wg(a.remap, T);
-      uint32_t lo = 0, hi = a.G - 1;  // the last group whose first task is <= u
-      while (lo < hi) {
-        const uint32_t mid = (lo + hi + 1) >> 1;
-        if (groups.first_task[mid] <= u) lo = mid; else hi = mid - 1;
+      const uint32_t full = __builtin_amdgcn_readfirstlane(groups.first_task[a.G]);
+      const uint32_t tails = __builtin_amdgcn_readfirstlane(groups.first_tail[a.G]) * loops_n;
+      if (blockIdx.x >= full + tails) return;  // the whole workgroup
+      if (blockIdx.x < full) {
+        const uint32_t u = logical_wg(a.remap, full);
+        g = find_group(groups.first_task, a.G, u);
+        t = block_coord((groups.first_row[g + 1] - groups.first_row[g]) / BM, loops_n, a.off, a.dir,
+                        u - groups.first_task[g]);
+        t.m = __builtin_amdgcn_readfirstlane(t.m);
+        t.n = __builtin_amdgcn_readfirstlane(t.n);
+      } else {
+        const uint32_t v = blockIdx.x - full;
+        g = find_group(groups.first_tail, a.G, v / loops_n);
+        t.m = __builtin_amdgcn_readfirstlane((groups.first_row[g + 1] - groups.first_row[g]) / BM);
+        t.n = v % loops_n;
       }
-      g = __builtin_amdgcn_readfirstlane(lo);
       row0 = __builtin_amdgcn_readfirstlane(groups.first_row[g]);
       rows = __builtin_amdgcn_readfirstlane(groups.first_row[g + 1]) - row0;
-      const uint32_t inner = __builtin_amdgcn_readfirstlane(u - groups.first_task[g]);
-      t = block_coord((rows + BM - 1) / BM, loops_n, a.off, a.dir, inner);
     } else {
       const uint32_t u = logical_wg(a.remap, a.grid);
       slice = a.mc.tiles.div(u);

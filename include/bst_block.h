@@ -22,6 +22,8 @@
  *    they may hold anything.  Other matrices (X, dY, C, dW, add) may have
  *    any element-aligned base and any pitch >= the row length; 16-byte
  *    aligned rows are faster.
+ *  - Outputs may not overlap inputs, except where a call says so.  Calls run on
+ *    the device that is current; operands, workspace and stream belong to it.
  *  - Sums are held in fp32 and rounded once to the output type, to nearest
  *    even.  Results do not depend on the schedule except for the order of
  *    the fp32 sums, and two calls with the same arguments give the same bits.
@@ -77,8 +79,8 @@ bst_status bst_dequant_block(bst_dtype x, int64_t M, int64_t K, int32_t block_ro
  *   trans_b = 1: B [N][ldb] (the transposed matrix), SB [ceil(N/128)][ldsb].
  *   The same weight in one storage order serves the forward product and, with
  *   the other value of trans_b, the gradient of the input (dX = dY . W^T).
- *   sa and sb are BST_E8M0 or BST_F32 each.  With BST_F32 the product of the
- *   two scales is formed in fp32 and must lie in its range.
+ *   sa and sb are BST_E8M0 or BST_F32 each.  The product of the two scales of
+ *   a sum must lie in the range of fp32.
  *   c: BST_BF16, BST_F16 or BST_F32.  The 8-bit matrix instructions behind
  *   bf16 and fp16 outputs add 8 consecutive products at the largest one's
  *   exponent and drop what is below 2^-13 of that (about 1.5e-5 of a result);

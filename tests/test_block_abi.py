@@ -202,7 +202,7 @@ def test_python_refuses_cpu_tensors():
 
 
 @pytest.mark.parametrize("tu", ["block_gemm_plain_t", "block_gemm_plain_n", "block_gemm_grouped_t",
-                                "block_gemm_grouped_n"])
+                                "block_gemm_grouped_n", "block"])
 def test_dma_scalar_operand_hazards(tu, tmp_path):
     """Every `buffer_load ... lds` sits right behind an `s_nop` of at least 4."""
     asm = str(tmp_path / "a.s")
@@ -219,4 +219,4 @@ def test_dma_scalar_operand_hazards(tu, tmp_path):
             m = re.match(r"s_nop (\d+)", prev)
             assert m and int(m.group(1)) >= 4, (prev, cur)
             found += 1
-    assert found > 100
+    assert found >= 32
