@@ -76,6 +76,7 @@ bst_status matrix_ok(const char* what, const void* p, int64_t ld, int64_t cols, 
   if (ld < cols)
     return set_error(BST_E_INVAL, "%s: leading dimension %lld below the row length %lld", what,
                      (long long)ld, (long long)cols);
+  if (ld > kSpan) return set_error(BST_E_INVAL, "%s: leading dimension above 2^31", what);
   if (!aligned(p, (uint64_t)es)) return set_error(BST_E_ALIGN, "%s is not aligned to its type", what);
   return BST_OK;
 }
@@ -122,7 +123,7 @@ struct Plan {
 bst_status plan_workspace(Plan& p, int64_t rows, int64_t N) {
   p.pitch = (uint32_t)(cdiv(N, 4) * 4);
   if (p.split > 1) {
-    if (rows * (p.pitch / 4) > 0xffffffffLL || N > kMaxSize - 8)
+    if (rows > 0xffffffffLL / std::max<int64_t>(p.pitch / 4, 1))
       return set_error(BST_E_INVAL, "a split output of %lld rows of %lld is too large",
                        (long long)rows, (long long)N);
     p.ws = (size_t)p.split * (size_t)rows * p.pitch * 4;
@@ -452,6 +453,8 @@ bst_status quant_args(BlockQuantArgs& a, bst_dtype x, int64_t M, int64_t K, int3
     return set_error(BST_E_INVAL, "leading dimension too small (ldx %lld, ldq %lld, K %lld, lds %lld, "
                      "blocks %lld)", (long long)ldx, (long long)ldq, (long long)K, (long long)lds,
                      (long long)kb);
+  if (ldx > kSpan || ldq > kSpan || lds > kSpan)
+    return set_error(BST_E_INVAL, "leading dimension above 2^31");
   if (M * kb > kMaxSize) return set_error(BST_E_INVAL, "more than 2^31-1 blocks");
   a.ldx = ldx;
   a.ldq = ldq;

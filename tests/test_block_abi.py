@@ -86,6 +86,7 @@ def test_quant_refusals(L):
     assert quant(L, ldx=255) == _lib.E_INVAL
     assert quant(L, ldq=255) == _lib.E_INVAL
     assert quant(L, lds=1) == _lib.E_INVAL
+    assert quant(L, ldx=1 << 32) == _lib.E_INVAL
     for k in ("X", "Q", "Sc"):
         assert quant(L, **{k: None}) == _lib.E_INVAL
         assert dequant(L, **{k: None}) == _lib.E_INVAL
@@ -120,6 +121,7 @@ def test_gemm_refusals(L):
     assert gemm(L, ldb=16 << 20) == _lib.E_UNSUPPORTED
     assert gemm(L, ldsa=8 << 20) == _lib.E_UNSUPPORTED
     assert gemm(L, ldc=255) == _lib.E_INVAL
+    assert gemm(L, ldc=1 << 40) == _lib.E_INVAL
     assert gemm(L, sched=S(tile=(96, 96))) == _lib.E_UNSUPPORTED
     assert gemm(L, c=FF, sched=S(tile=(256, 256))) == _lib.E_UNSUPPORTED    # 16-bit outputs only
     assert gemm(L, sched=S(offset=0)) == _lib.E_INVAL
@@ -149,6 +151,11 @@ def test_workspace(L):
     assert L.bst_block_workspace_bytes(0, 1, 1, 512, 16384, None) > 0
     assert L.bst_block_workspace_bytes(3, 1, 1, 512, 16384, None) == 0    # few rows: one launch
     assert L.bst_block_workspace_bytes(0, 1, 1, 512, 2048, None) == 0
+    # partial sums past what the last addition indexes are refused, not wrapped
+    g = bst.make_sched(tile=(128, 128), split_k=2)
+    assert L.bst_block_workspace_bytes(2, 1024, 1 << 20, (1 << 31) - 1, (1 << 31) - 1, ctypes.byref(g)) == 0
+    assert L.bst_block_workspace_bytes(1, 1, 1 << 20, 1 << 20, 1 << 20, ctypes.byref(g)) == 0
+    assert L.bst_block_workspace_bytes(0, 1, 64, 0, 4096, None) == 0
     # a split never has an empty slice: 3 blocks of K cut 8 ways are 3 slices
     s = bst.make_sched(tile=(64, 128), split_k=8)
     assert L.bst_block_workspace_bytes(0, 1, 64, 256, 384, ctypes.byref(s)) == 3 * 64 * 256 * 4

@@ -13,6 +13,7 @@ less than 7 * 2^-13 * 2^(largest exponent of its 8 A codes + largest of its 8 B 
 restored values are exact by definition and compared bit for bit."""
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -335,6 +336,15 @@ def test_product_nan_and_zero():
                               e(3, 0, device="cuda", dtype=torch.uint8),
                               e(0, 1, device="cuda", dtype=torch.uint8))
     assert z.shape == (3, 5) and bool((z == 0).all())
+    for M, out in ((70, BF), (70, FF), (300, BF)):      # K = 0 on the tiles, plain and grouped
+        q, s = e(M, 0, device="cuda").to(torch.float8_e4m3fn), e(M, 0, device="cuda", dtype=torch.uint8)
+        for tb in (False, True):
+            shape, sshape = ((200, 0), (2, 0)) if tb else ((0, 200), (0, 2))
+            w = e(3, *shape, device="cuda").to(torch.float8_e4m3fn)
+            ws = e(3, *sshape, device="cuda", dtype=torch.uint8)
+            gm = torch.tensor([M - 10, 0, 10], dtype=torch.int32, device="cuda")
+            assert bool((bst.gemm_block_scaled(q, w[0], s, ws[0], trans_b=tb, out_dtype=out) == 0).all())
+            assert bool((bst.grouped_gemm_block_scaled(q, w, gm, s, ws, trans_b=tb, out_dtype=out) == 0).all())
     A, sa, B, sb = operands(4, 16, 128, False, KINDS[0], gen(9))
     assert bst.gemm_block_scaled(A[:0], B, sa[:0], sb).shape == (0, 16)
     sa[2] = 255
@@ -472,6 +482,69 @@ def test_grouped_weight_grad(dtype):
                           2 * (hi - lo) + 1, FF)
                 if hi == lo:
                     assert torch.equal(dA[k], add[k]) and bool((dW[k] == 0).all())
+
+
+# -------------------------------------------------- calls of every kind ---
+@pytest.mark.parametrize("seed", range(8))
+def test_seeded_calls(seed):
+    """Twelve calls a seed over the whole range of sizes, layouts, scale and output types and
+    schedules, each against its definition."""
+    r = random.Random(seed)
+
+    def size(top):
+        n = int(round(math.exp(r.uniform(0, math.log(top)))))
+        return r.choice([n, -(-n // 8) * 8, -(-n // 128) * 128])
+    for _ in range(12):
+        g = gen(r.randrange(1 << 30))
+        op = r.choice(["product", "product", "grouped", "grad", "ggrad"])
+        M, N, K = size(900), size(900), size(900)
+        G = r.choice([1, 2, 5, 17])
+        cuts = sorted(r.randrange(M + 1) for _ in range(G))
+        sizes = [b - a for a, b in zip([0] + cuts[:-1], cuts)]
+        gm = torch.tensor(sizes, dtype=torch.int32, device="cuda")
+        direction, offset, remap = r.choice(["zn", "nz", "raster"]), r.choice([1, 2, 7]), r.choice([0, 1])
+        kw = dict(offset=offset, direction=direction, xcd_remap=remap)
+        if op in ("product", "grouped"):
+            tb, kinds, out = r.choice([False, True]), r.choice(KINDS), r.choice([BF, HF, FF])
+            tile = r.choice([None, None, (0, 0)] + [t for t in TILES if out != FF or t[0] < 256])
+            split = r.choice([0, 1, 2, 7]) if op == "product" else r.choice([0, 1])
+            sched = None if tile is None else bst.make_sched(tile=tile, split_k=split, **kw)
+            say(op, M, N, K, tb, kinds, out, tile, split, kw, sizes if op == "grouped" else "")
+            A, sa, B, sb = operands(M, N, K, tb, kinds, g, G=G if op == "grouped" else 0,
+                                    extra=r.choice([0, 16, 48]))
+            if op == "product":
+                C = bst.gemm_block_scaled(A, B, sa, sb, trans_b=tb, out_dtype=out, sched=sched)
+                ref, den = ref_product(A, sa, B, sb, tb)
+                check_sum(C, ref, den, K, out, op, cut_product(A, sa, B, sb, tb))
+                continue
+            C = torch.full((M, N), 7.0, dtype=out, device="cuda")
+            bst.grouped_gemm_block_scaled(A, B, gm, sa, sb, C, trans_b=tb, sched=sched)
+            for k, (lo, hi) in enumerate(spans(sizes, M)):
+                if hi > lo:
+                    ref, den = ref_product(A[lo:hi], sa[lo:hi], B[k], sb[k], tb)
+                    check_sum(C[lo:hi], ref, den, K, out, op, cut_product(A[lo:hi], sa[lo:hi], B[k], sb[k], tb))
+            assert bool((C[cuts[-1]:] == 7).all())
+            continue
+        dtype, out = r.choice([BF, HF, FF]), r.choice([BF, HF, FF])
+        tile, split = r.choice([None, (0, 0), (128, 128), (256, 256)]), r.choice([0, 1, 2, 5])
+        sched = None if tile is None else bst.make_sched(tile=tile, split_k=split, **kw)
+        say(op, M, N, K, dtype, out, tile, split, kw, sizes if op == "ggrad" else "")
+        q, s = kept(M, K, g)
+        dY = grads(M, N, dtype, g, r.choice([True, False]))
+        shape = (K, N) if op == "grad" else (G, K, N)
+        add = r.choice([None, torch.randn(shape, generator=g, device="cuda").to(out)])
+        parts = {BF: 1, HF: 2, FF: 3}[dtype]
+        if op == "grad":
+            dW = bst.weight_grad(q, s, dY, add=add, out_dtype=out, sched=sched)[None]
+        else:
+            dW = bst.grouped_weight_grad(q, s, dY, gm, add=add, out_dtype=out, sched=sched)
+        for k, (lo, hi) in enumerate([(0, M)] if op == "grad" else spans(sizes, M)):
+            x, d = wide(q, s)[lo:hi], dY[lo:hi].double()
+            ref, den = x.t() @ d, x.abs().t() @ d.abs()
+            if add is not None:
+                more = (add[None] if op == "grad" else add)[k].double()
+                ref, den = ref + more, den + more.abs()
+            check_sum(dW[k], ref, den, parts * (hi - lo) + 1, out, op)
 
 
 # ------------------------------------------------ together, as they are used ---
