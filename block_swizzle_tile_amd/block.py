@@ -22,10 +22,13 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
-from ._lib import BF16, F16, F32, Sched, check, lib
+from ._lib import BF16, F16, F32, PKG, Sched, check, lib
 
 E8M0 = 8
 
@@ -39,6 +42,28 @@ _CODES = torch.float8_e4m3fn
 
 
 _L = None
+_fast_module = None
+FAST_PATH = os.path.join(PKG, "_block_fast.so")
+
+
+def _fast():
+    """csrc/block_fast.cpp: the short way for calls with new outputs on the current device.  Its
+    functions answer None to what they do not take, and the checks here say why."""
+    return _fast_module or _load_fast()
+
+
+def _load_fast():
+    global _fast_module
+    if not os.path.exists(FAST_PATH):
+        raise RuntimeError("_block_fast.so is not built (%s); run "
+                           "`python -m block_swizzle_tile_amd.build`" % FAST_PATH)
+    loader = importlib.machinery.ExtensionFileLoader("_block_fast", FAST_PATH)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_block_fast", loader))
+    loader.exec_module(m)
+    L = _bound()
+    m.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in BLOCK_EXPORTS])
+    _fast_module = m
+    return m
 
 
 def _bound():
@@ -200,6 +225,10 @@ def quant_block(X, Q=None, scale=None, *, block_rows=1):
     16 != 0 it is a view of a wider matrix.  Rounding is to nearest even under the smallest
     power-of-two scale that holds the block's largest finite magnitude; infinities and NaN become
     NaN (bst_quant_block)."""
+    if Q is None and scale is None:
+        out = _fast().quant(X, block_rows)
+        if out is not None:
+            return out
     d = _device(X, Q, scale)
     if d != _current_device():
         return _elsewhere(_quant)(d, X, Q, scale, block_rows)
@@ -231,6 +260,10 @@ def _dequant(d, Q, scale, X, out_dtype, block_rows):
 def dequant_block(Q, scale, X=None, *, out_dtype=None, block_rows=1):
     """The matrix that codes Q and scales stand for, in out_dtype (bf16 by default; bf16, fp16 or
     fp32); finite values past the type's range give its largest (bst_dequant_block)."""
+    if X is None:
+        out = _fast().dequant(Q, scale, out_dtype, block_rows)
+        if out is not None:
+            return out
     d = _device(Q, scale, X)
     if d != _current_device():
         return _elsewhere(_dequant)(d, Q, scale, X, out_dtype, block_rows)
@@ -270,8 +303,13 @@ def gemm_block_scaled(A, B, scale_a, scale_b, C=None, *, trans_b=False, out_dtyp
 
     A [M][K] with scale_a [M][ceil(K/128)]; B [K][N] with scale_b [ceil(K/128)][ceil(N/128)], or
     with trans_b B [N][K] and scale_b [ceil(N/128)][ceil(K/128)] (bst_gemm_block_scaled)."""
+    trans_b = bool(trans_b)
+    if C is None and sched is None and workspace is None:
+        out = _fast().gemm(A, B, scale_a, scale_b, trans_b, out_dtype)
+        if out is not None:
+            return out
     d = _device(A, B, scale_a, scale_b, C)
-    args = (d, A, B, scale_a, scale_b, C, bool(trans_b), out_dtype, sched, workspace)
+    args = (d, A, B, scale_a, scale_b, C, trans_b, out_dtype, sched, workspace)
     return _gemm(*args) if d == _current_device() else _elsewhere(_gemm)(*args)
 
 
@@ -301,8 +339,13 @@ def grouped_gemm_block_scaled(A, B, group_m, scale_a, scale_b, C=None, *, trans_
     """Groups of rows stacked along M, each times its own B[g]: group_m is a device int32 vector of
     row counts (never read on the host).  Rows of C past the last group are left as they were
     (unset in a new C) (bst_grouped_gemm_block_scaled)."""
+    trans_b = bool(trans_b)
+    if C is None and sched is None:
+        out = _fast().grouped(A, B, group_m, scale_a, scale_b, trans_b, out_dtype)
+        if out is not None:
+            return out
     d = _device(A, B, group_m, scale_a, scale_b, C)
-    args = (d, A, B, group_m, scale_a, scale_b, C, bool(trans_b), out_dtype, sched)
+    args = (d, A, B, group_m, scale_a, scale_b, C, trans_b, out_dtype, sched)
     return _grouped(*args) if d == _current_device() else _elsewhere(_grouped)(*args)
 
 
@@ -347,6 +390,10 @@ def weight_grad(Q, scale, dY, dW=None, *, add=None, out_dtype=None, sched=None, 
     scales) and dY [M][N] in bf16, fp16 or fp32; no operand is rounded, sums are fp32.  add: dW's
     dtype and shape, may be dW itself (gradient accumulation).  fp32 out by default
     (bst_weight_grad)."""
+    if dW is None and sched is None and workspace is None:
+        out = _fast().grad(Q, scale, dY, None, add, out_dtype)
+        if out is not None:
+            return out
     d = _device(Q, scale, dY, dW, add)
     args = (d, Q, scale, dY, dW, add, out_dtype, sched, workspace)
     return _grad(*args) if d == _current_device() else _elsewhere(_grad)(*args)
@@ -369,6 +416,10 @@ def grouped_weight_grad(Q, scale, dY, group_m, dW=None, *, add=None, out_dtype=N
                         workspace=None):
     """weight_grad over each group of rows: dW [G][K][N], group_m a device int32 vector of row
     counts; an empty group's gradient is its add (or zeros) (bst_grouped_weight_grad)."""
+    if dW is None and sched is None and workspace is None:
+        out = _fast().grad(Q, scale, dY, group_m, add, out_dtype)
+        if out is not None:
+            return out
     d = _device(Q, scale, dY, group_m, dW, add)
     args = (d, Q, scale, dY, group_m, dW, add, out_dtype, sched, workspace)
     return _grouped_grad(*args) if d == _current_device() else _elsewhere(_grouped_grad)(*args)

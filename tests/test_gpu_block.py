@@ -660,6 +660,61 @@ def test_streams_and_graphs():
             assert torch.equal(y, ref) and torch.equal(acc, once), r
 
 
+def test_short_way_equals_the_long_one():
+    """Calls with new outputs go through one C function: it takes them, gives the bits of the path
+    with given outputs, leaves nothing allocated behind, and answers None to what it does not take."""
+    f = blk._fast()
+    M, N, K, G = 77, 136, 264, 3
+    g = gen(31)
+    x = torch.randn(M, K, generator=g, device="cuda").to(BF)
+    for br in (1, 128):
+        q, s = f.quant(x, br)
+        q2, s2 = bst.quant_block(x, torch.empty(M, 272, device="cuda").to(torch.float8_e4m3fn)[:, :K],
+                                 torch.empty_like(s), block_rows=br)
+        assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+        assert q.stride() == (272, 1) and q.shape == (M, K)
+        y = f.dequant(q, s, HF, br)
+        assert torch.equal(y, bst.dequant_block(q, s, torch.empty_like(y), block_rows=br))
+        assert f.dequant(q, s, None, br).dtype == BF
+    q, s = f.quant(x, 1)
+    gm = torch.tensor([50, 0, 27], dtype=torch.int32, device="cuda")
+    dy = torch.randn(M, N, generator=g, device="cuda").to(HF)
+    for tb in (False, True):
+        _, _, B, sb = operands(1, N, K, tb, ("e8m0", "f32"), g, G=G)
+        c = f.gemm(q, B[0], s, sb[0], tb, HF)
+        assert torch.equal(c, bst.gemm_block_scaled(q, B[0], s, sb[0], torch.empty_like(c), trans_b=tb))
+        c = f.grouped(q, B, gm, s, sb, tb, None)
+        assert torch.equal(c, bst.grouped_gemm_block_scaled(q, B, gm, s, sb, torch.empty_like(c), trans_b=tb))
+    add = torch.randn(G, K, N, generator=g, device="cuda").to(BF)
+    w = f.grad(q, s, dy, None, add[0], None)
+    assert w.dtype == BF and torch.equal(w, bst.weight_grad(q, s, dy, torch.empty_like(w), add=add[0]))
+    w = f.grad(q, s, dy, gm, add, BF)
+    assert torch.equal(w, bst.grouped_weight_grad(q, s, dy, gm, torch.empty_like(w), add=add))
+    w = f.grad(q, s, dy, None, None, None)
+    assert w.dtype == FF and torch.equal(w, bst.weight_grad(q, s, dy, torch.empty_like(w)))
+    # not taken: wrong types, shapes, places, numbers and kinds of arguments
+    assert f.quant(x.cpu(), 1) is None and f.quant(x, 2) is None and f.quant(x) is None
+    assert f.quant(x.t(), 1) is None and f.quant(x.int(), 1) is None and f.quant(3, 1) is None
+    assert f.quant(x, "1") is None and f.dequant(x, s, None, 1) is None
+    assert f.dequant(q, s, "bf16", 1) is None and f.dequant(q, s[:, :1], None, 1) is None
+    assert f.gemm(q, B[0], s, sb, True, None) is None and f.gemm(q, B, s, sb[0], True, None) is None
+    assert f.gemm(q, B[0], s, sb[0], True, torch.int8) is None
+    assert f.grouped(q, B, gm.long(), s, sb, True, None) is None
+    assert f.grad(q, s, dy[:, 0], None, None, None) is None and f.grad(q, s, dy, gm, add[0], None) is None
+    assert f.grad(q, s.float(), dy, None, None, None) is None and f.grad(q, s, dy, None, add[0], FF) is None
+
+    def held():
+        for _ in range(50):
+            f.quant(x, 1)
+            f.gemm(q, B[0], s, sb[0], True, None)
+            f.grad(q, s, dy, gm, add, None)
+            f.gemm(q, B[0], s, sb, True, None)
+        torch.cuda.synchronize()
+        return torch.cuda.memory_allocated()
+    first, second = held(), held()
+    assert first == second
+
+
 def test_noncurrent_stream_pointer_and_refusals():
     A, sa, B, sb = operands(40, 64, 256, False, KINDS[0], gen(1))
     with pytest.raises(ValueError):
