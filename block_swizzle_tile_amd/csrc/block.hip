@@ -216,14 +216,14 @@ bst_status plan_grad(int64_t count, int64_t M, int64_t N, int64_t K, const Sched
 // all of K, so they lose to a split where K is long or the rows fill more
 // operands.  Weights N x K: 16 rows 7.1 us against 10.3 (4096 x 4096), 18.5
 // against 16.2 at K = 14336; 32 rows 9.9 against 10.3 and 27.7 against 17.
-// Weights K x N: one row 7.1 us against 9.2 (4096 x 4096), 31 against 15 at K =
-// 14336; 33 rows 9.2 against 10.6 at K = 2056 and 12.0 against 11.7 at 4096;
-// and past 16384 columns the tiles fill the chip unsplit (16.5 against 14.8).
+// Weights K x N: one row 7.0 us against 9.2 (4096 x 4096) and 9.6 against 10.5 at
+// K = 8192; 33 rows 7.0 against 10.6 at K = 2056 and 11.4 against 11.7 at 4096;
+// and from 16384 columns on the tiles fill the chip unsplit.
 bool takes_rows(int32_t trans_b, int64_t M, int64_t N, int64_t K, const Sched& s) {
   if (s.tm != 0 || s.tn != 0 || s.split != 0) return false;
   const int64_t nk = cdiv(K, 128);
   if (trans_b) return M <= 16 || (M <= 32 && nk <= 32);
-  return M <= 64 && cdiv(nk, 8) * cdiv(M, 32) <= 6 && cdiv(N, 128) * 2 < device_cu_count();
+  return M <= 64 && cdiv(nk, 8) * cdiv(M, 32) <= 8 && cdiv(N, 128) * 2 < device_cu_count();
 }
 
 bst_status check_ws(const Plan& p, const void* ws, size_t bytes) {
@@ -335,7 +335,7 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
   a.cvec = vec_rows(C, ldc, 0, out_bytes(c));
   if (rows) {
     const int fn = cdiv(N, 32) >= 2 * device_cu_count() ? 2 : 1;
-    a.grid = (uint32_t)cdiv(N, trans_b ? 16 * fn : 64);
+    a.grid = (uint32_t)cdiv(N, trans_b ? 16 * fn : 32);
     const dim3 grid(a.grid), block(512);
     auto run = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, block, 0, (hipStream_t)stream, a);

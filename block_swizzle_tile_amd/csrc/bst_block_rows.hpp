@@ -143,14 +143,17 @@ __global__ void __launch_bounds__(512) block_rows_kernel(BlockGemmArgs a) {
 // ------------------------------------------------------- weights K x N ----
 // The same for weights whose rows run along N: an operand then has to be
 // gathered from 128 rows, which the transposing LDS reads do.  A workgroup
-// takes 64 columns; its eight waves share out the blocks of K, and each runs
-// a pipeline of its own (DMA of the wave's next 128 x 64 patch into its own
+// takes 32 columns; its eight waves share out the blocks of K, and each runs
+// a pipeline of its own (DMA of the wave's next 128 x 32 patch into its own
 // two LDS buffers while it multiplies the last one), so that the loop has no
-// barrier and eight patches are in flight per CU.  A comes straight from
-// memory: a lane's 32 bytes of each half block.
+// barrier and eight patches are in flight per workgroup.  The 32-byte rows of
+// a patch share their cache lines with the neighbours', which run on the same
+// die.  64 columns were slower (33 rows, 4112 x 2056: 8.4 us against 7.0), and
+// so were 16 waves (9.8).  A comes straight from memory: a lane's 32 bytes of
+// each half block.
 template <int FM, bool EXACT>
 struct BlockRowsN {
-  static constexpr int NW = 8, BN = 64, FN = 2;
+  static constexpr int NW = 8, BN = 32;
   static constexpr int BUF = 128 * BN;  // a patch
   static constexpr int SUMS = FM * 32 * BN * 4;  // a wave's partial sums
   static constexpr int LDS_BYTES = NW * (2 * BUF > SUMS ? 2 * BUF : SUMS);
@@ -161,8 +164,9 @@ struct BlockRowsN {
     __shared__ __attribute__((aligned(16))) uint8_t buf[LDS_BYTES];
     return (lds_t*)buf;
   }
-  // XOR of a row's four chunks: rows 0..7 of a transposing read fall on all banks
-  static __device__ __forceinline__ uint32_t swz_n(uint32_t k) { return (k >> 1) & 3u; }
+  // XOR of a row's chunks: rows 0..7 of a transposing read fall on all banks
+  static constexpr int CPR = BN / 16, RPI = 64 / CPR, DMAS = 128 / RPI;
+  static __device__ __forceinline__ uint32_t swz_n(uint32_t k) { return (k >> 2) & 1u; }
 
   struct Next {
     i32x8_t a[2][FM];
@@ -174,25 +178,22 @@ struct BlockRowsN {
     const uint32_t l32 = lane & 31u, hi = lane >> 5;
     const uint32_t n0 = logical_wg(1u, a.grid) * BN;
     const uint32_t cols = a.N - n0 < (uint32_t)BN ? a.N - n0 : BN;
-    const int64_t sb = n0 / kScaleBlock;  // one block of columns: 64 divides 128
+    const int64_t sb = n0 / kScaleBlock;  // one block of columns: 32 divides 128
     lds_t* const own = lds() + wave * (2 * BUF);
-    // DMA instruction x: K rows 16 x + lane / 4, chunk lane % 4 of the patch
-    const uint32_t dk = lane >> 2, dch = (lane & 3u) ^ swz_n(dk);
+    // DMA instruction x: K rows RPI x + lane / CPR, chunk lane % CPR of the patch
+    const uint32_t dk = lane / CPR, dch = (lane % CPR) ^ swz_n(dk);
     const uint32_t doff = dch * 16 < cols ? dk * (uint32_t)a.ldb + dch * 16 : kOob;
     // transposing reads: K = 64 kk + 32 (t >> 1) + 16 hi + 8 (t & 1) + (L >> 1)
     const uint32_t L = lane & 15u, rk = 16 * hi + (L >> 1);
-    uint32_t roff[FN];
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-      roff[j] = rk * BN + (((2 * j + ((lane >> 4) & 1u)) ^ swz_n(rk)) << 4) + 8 * (L & 1u);
+    const uint32_t roff = rk * BN + ((((lane >> 4) & 1u) ^ swz_n(rk)) << 4) + 8 * (L & 1u);
 
     auto fetch = [&](uint32_t kb, uint32_t s, Next& n) {
       const uint32_t left = a.K - kb * 128u;  // > 0
       const u32x4_t d = make_desc(a.B + (int64_t)kb * 128 * a.ldb + n0);
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        dma16(d, own + s * BUF + x * 1024, 16 * x + dk < left ? doff : kOob,
-              16u * x * (uint32_t)a.ldb);
+      for (int x = 0; x < DMAS; ++x)
+        dma16(d, own + s * BUF + x * 1024, RPI * x + dk < left ? doff : kOob,
+              (uint32_t)(RPI * x) * (uint32_t)a.ldb);
       const float fb = Rows::scale(a.sb, sb + (int64_t)kb * a.ldsb, a.sb_f32 != 0);
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
@@ -212,13 +213,11 @@ struct BlockRowsN {
       }
     };
 
-    f32x16_t acc[FM][FN];
+    f32x16_t acc[FM];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+      for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
     Next next;
     uint32_t s = 0;
     if (wave < a.nk) fetch(wave, 0, next);
@@ -226,63 +225,56 @@ struct BlockRowsN {
       const Next now = next;
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this patch has landed
       if (kb + NW < a.nk) fetch(kb + NW, s ^ 1u, next);
-      i32x8_t b[2][FN];
+      i32x8_t b[2];
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
+      for (int kk = 0; kk < 2; ++kk) {
+        i32x2_t v[4];
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          i32x2_t v[4];
+        for (int t = 0; t < 4; ++t)
+          v[t] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (lds_i32x2_t*)(own + s * BUF + roff + (64 * kk + 32 * (t >> 1) + 8 * (t & 1)) * BN));
+        b[kk] = i32x8_t{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
+      }
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
-            v[t] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                (lds_i32x2_t*)(own + s * BUF + roff[j] + (64 * kk + 32 * (t >> 1) + 8 * (t & 1)) * BN));
-          b[kk][j] = i32x8_t{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
-        }
+      for (int i = 0; i < FM; ++i) {
+        f32x16_t p = {};
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+        for (int kk = 0; kk < 2; ++kk) {
+          if constexpr (EXACT) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          f32x16_t p = {};
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {
-            if constexpr (EXACT) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_codes(b[kk][j], u),
-                                                            widen_codes(now.a[kk][i], u), p, 0, 0, 0);
-            } else {
-              p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[kk][j], now.a[kk][i], p, 0, 0, 0,
-                                                                  0, 0, 0);
-            }
+            for (int u = 0; u < 4; ++u)
+              p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_codes(b[kk], u),
+                                                          widen_codes(now.a[kk][i], u), p, 0, 0, 0);
+          } else {
+            p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[kk], now.a[kk][i], p, 0, 0, 0, 0,
+                                                                0, 0);
           }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(now.f[i], p[e], acc[i][j][e]);
         }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] = __builtin_fmaf(now.f[i], p[e], acc[i][e]);
+      }
       s ^= 1u;
     }
-    // ---- the waves' sums, each in rows of 64 columns whose 4-column chunks
+    // ---- the waves' sums, each in rows of BN columns whose 4-column chunks
     // are XORed by the row, then added in wave order
+    constexpr uint32_t QPR = BN / 4;
     __syncthreads();
     typedef __attribute__((address_space(3))) f32x4_t lds_f4_t;
     lds_t* const mine = lds() + wave * SUMS;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t m = i * 32 + l32, ch = 8 * j + 2 * q + hi;
-          *(lds_f4_t*)(mine + m * (BN * 4) + ((ch ^ (m & 15u)) << 4)) =
-              f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                      acc[i][j][4 * q + 3]};
-        }
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t m = i * 32 + l32, ch = 2 * q + hi;
+        *(lds_f4_t*)(mine + m * (BN * 4) + ((ch ^ (m & (QPR - 1))) << 4)) =
+            f32x4_t{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
+      }
     __syncthreads();
     const int64_t es = a.ckind == OUT_F32 ? 4 : 2;
-#pragma unroll
-    for (int o = 0; o < FM; ++o) {
-      const uint32_t id = o * 512 + threadIdx.x, m = id / 16, ch = id % 16, c = ch * 4;
+    for (uint32_t id = threadIdx.x; id < FM * 32 * QPR; id += NW * 64) {
+      const uint32_t m = id / QPR, ch = id % QPR, c = ch * 4;
       if (m >= a.M || c >= cols) continue;
-      const lds_t* p = lds() + m * (BN * 4) + ((ch ^ (m & 15u)) << 4);
+      const lds_t* p = lds() + m * (BN * 4) + ((ch ^ (m & (QPR - 1))) << 4);
       f32x4_t t = *(const lds_f4_t*)p;
 #pragma unroll
       for (int w = 1; w < NW; ++w) t += *(const lds_f4_t*)(p + w * SUMS);
