@@ -198,7 +198,7 @@ bst_status plan_grad(int64_t count, int64_t M, int64_t N, int64_t K, const Sched
     const double stage = p.tm == 128 ? 1.5 : 2.0, slice = (double)G * K * N * 8 / 5e6;
     const int64_t at_once = p.tm == 128 ? 2 * cus : cus;
     double best = 0;
-    for (int64_t n = 1; n <= std::min<int64_t>(16, std::max<int64_t>(stages, 1)); ++n) {
+    for (int64_t n = 1; n <= std::min<int64_t>(32, std::max<int64_t>(stages, 1)); ++n) {
       const double cost = cdiv(p.tiles * n, at_once) * cdiv(stages, n) * stage +
                           (n > 1 ? n * slice + 2 : 0);
       if (split == 0 || cost < best) {

@@ -249,14 +249,29 @@ static __global__ void __launch_bounds__(256) sum_partials(ReduceArgs a) {
     const uint32_t rr = a.quads.div(i), q = i - rr * a.quads.d;
     const uint32_t g = a.by_rows.div(rr), r = rr - g * a.rows;
     const float* p = a.part + (int64_t)i * 4;
+    // in slice order, eight slices in flight
     f32x4_t s = *(const f32x4_t*)p;
-    for (uint32_t k = 1; k < a.split; ++k) s += *(const f32x4_t*)(p + k * slice);
+    uint32_t k = 1;
+    for (; k + 8 <= a.split; k += 8) {
+      f32x4_t v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = *(const f32x4_t*)(p + (k + u) * slice);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
+    f32x4_t v[7];
+#pragma unroll
+    for (int u = 0; u < 7; ++u)
+      if (k + u < a.split) v[u] = *(const f32x4_t*)(p + (k + u) * slice);
+#pragma unroll
+    for (int u = 0; u < 7; ++u)
+      if (k + u < a.split) s += v[u];
     const uint32_t n = q * 4;
     if (n >= a.cols) continue;
-    float v[4] = {s[0], s[1], s[2], s[3]};
+    float w[4] = {s[0], s[1], s[2], s[3]};
     uint8_t* d = a.dst + (g * a.stride + r * a.ld + n) * es;
     const uint8_t* ad = a.add ? a.add + (g * a.strideadd + r * a.ldadd + n) * es : nullptr;
-    put_run<4>(d, ad, v, a.cols - n, a.vec && a.cols - n >= 4u, a.kind);
+    put_run<4>(d, ad, w, a.cols - n, a.vec && a.cols - n >= 4u, a.kind);
   }
 }
 
