@@ -4,7 +4,8 @@
 //
 // The sum runs over rows, and every row has its own scales, so they cannot
 // leave the sum: x is restored on its way into LDS.  A code times a power of
-// two is exact in bf16 (4 significant bits of 8), one conversion instruction
+// two is exact in bf16 (4 significant bits of 8; past the type's end it is the
+// largest value, as bst_dequant_block gives it), one conversion instruction
 // makes two of them, and each is made once per workgroup.  dY joins as bf16:
 // as it is, or as 2 (fp16) or 3 (fp32) bf16 parts that add up to it, each
 // with its own matrix product, so that nothing is rounded before the fp32
@@ -52,6 +53,15 @@ __device__ __forceinline__ uint32_t take_part(float& f) {
     f -= __builtin_bit_cast(float, h);
   }
   return h >> 16;
+}
+
+// Two bf16 whose infinities become the largest finite value, as when restoring:
+// 256 * 2^120, the code of values within half a step of the type's end, is past
+// it, and a zero gradient times an infinity would be NaN.  Only scale bytes of
+// 247 and more reach that far.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+  w -= (w & 0x7fffu) == 0x7f80u ? 1u : 0u;
+  return w - ((w & 0x7fff0000u) == 0x7f800000u ? 0x10000u : 0u);
 }
 
 template <int BK, int BN, int WM, int WN, int DY>
@@ -151,6 +161,10 @@ struct BlockGrad {
         const b2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(h.x[i][d], s, true);
         o[2 * d] = __builtin_bit_cast(uint32_t, lo);
         o[2 * d + 1] = __builtin_bit_cast(uint32_t, hi);
+      }
+      if (h.e[i] >= 247u) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d) o[d] = finite_pair(o[d]);
       }
       lds_t* row = base + r * XB;
       const uint32_t z = swz_r<XB>(r);

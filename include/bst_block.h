@@ -130,9 +130,11 @@ bst_status bst_grouped_gemm_block_scaled(bst_dtype c, int32_t trans_b, int32_t G
  * bst_quant_block with block_rows = 1 made (codes Q [M][ldq], E8M0 scales
  * S [M][lds]), dY [M][lddy] is the output's gradient in bf16, fp16 or fp32.
  *   dW[k][n] = add[k][n] + sum over m of X[m][k] * dY[m][n].
- *   X is exact in bf16 and the products run on bf16 matrix instructions: a
- *   bf16 dY as it is, an fp16 or fp32 dY as two or three bf16 parts that add
- *   up to it (exactly, down to 2^-133), so no operand is rounded.
+ *   X is what bst_dequant_block gives in bf16: exact above 2^-133, and where a
+ *   code times its scale is past bf16's range, bf16's largest value.  The
+ *   products run on bf16 matrix instructions: a bf16 dY as it is, an fp16 or
+ *   fp32 dY as two or three bf16 parts that add up to it (exactly, down to
+ *   2^-133), so no operand is rounded.
  *   dw: BST_F32, BST_BF16 or BST_F16.  add_dev: NULL, or a matrix of dW's
  *   type and layout ([K][ldadd]); it may be dW itself.  M = 0 gives add (or 0).
  *   tile_m x tile_n of sched: 128x128 or 256x256 (tile_m along K, tile_k 0);

@@ -456,6 +456,31 @@ def test_weight_grad_empty_and_special():
     assert torch.equal(bst.weight_grad(q, s, dY), v.expand(16, 4))
 
 
+@pytest.mark.parametrize("dtype", [BF, FF])
+def test_weight_grad_of_extreme_activations(dtype):
+    """Activations at the ends of the type's range (a mask's lowest value among them): the largest
+    may round up to a code whose value, 2^128, is past bf16, and then stands for bf16's largest, as
+    in restoring; it never becomes infinite, so a zero gradient beside it contributes nothing."""
+    g = gen(77)
+    M, K, N = 70, 272, 40
+    x = torch.randn(M, K, generator=g, device="cuda", dtype=FF).to(dtype)
+    top = torch.finfo(dtype).max
+    x[0, 0], x[1, 5], x[2, 130], x[3, 271] = top, -top, top * 0.9375, -top * 0.5
+    q, s = bst.quant_block(x)
+    s = s.clone()
+    s[4] = 254                                              # scales from elsewhere
+    q.view(torch.uint8)[4, 128:] = 0x7e
+    r = bst.dequant_block(q, s)
+    assert bool(r.isfinite().all()) and int(s.max()) >= 247
+    dy = torch.randn(M, N, generator=g, device="cuda", dtype=FF).to(dtype) * 2.0 ** -30
+    dy[:5, ::2] = 0.0
+    w = bst.weight_grad(q, s, dy)
+    ref, den = r.double().t() @ dy.double(), r.double().abs().t() @ dy.double().abs()
+    parts = {BF: 1, FF: 3}[dtype]
+    check_sum(w, ref, den, M * parts, FF)
+    say("extreme activations", dtype)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_grouped_weight_grad(dtype):
     for sizes, total in GROUPS:
