@@ -86,6 +86,13 @@ bst_status launched(hipError_t e, const char* what) {
   return set_error(BST_E_HIP, "%s launch failed: %s", what, hipGetErrorString(e));
 }
 
+// A launch holds fewer than 2^32 threads.
+bst_status grid_ok(int64_t workgroups, int64_t threads) {
+  if (workgroups <= 0xffffffffLL / threads) return BST_OK;
+  return set_error(BST_E_UNSUPPORTED, "%lld workgroups of %lld threads are more than one launch holds",
+                   (long long)workgroups, (long long)threads);
+}
+
 // ------------------------------------------------------------ schedule ----
 struct Sched {
   uint32_t tm = 0, tn = 0, off = 8, dir = BST_ZN, remap = 1, split = 0;
@@ -123,14 +130,13 @@ struct Plan {
 bst_status plan_workspace(Plan& p, int64_t rows, int64_t N) {
   p.pitch = (uint32_t)(cdiv(N, 4) * 4);
   if (p.split > 1) {
-    if (rows > 0xffffffffLL / std::max<int64_t>(p.pitch / 4, 1))
+    // sum_partials counts quads, and a grid's worth past the last, in 32 bits
+    if (rows > kMaxSize / std::max<int64_t>(p.pitch / 4, 1))
       return set_error(BST_E_INVAL, "a split output of %lld rows of %lld is too large",
                        (long long)rows, (long long)N);
     p.ws = (size_t)p.split * (size_t)rows * p.pitch * 4;
   }
-  if (p.tiles * p.split > kMaxSize)
-    return set_error(BST_E_INVAL, "task count above 2^31-1");
-  return BST_OK;
+  return grid_ok(p.tiles * p.split, 512);
 }
 
 // Tile and split of a product.  count: groups (0: plain); exact: an fp32 output.
@@ -291,7 +297,11 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
   }
   const bool rows = !grouped && takes_rows(trans_b, M, N, K, s);
   Plan p;
-  if (!rows) {
+  const int fn = cdiv(N, 32) >= 2 * device_cu_count() ? 2 : 1;  // a rows kernel's operands of B
+  const int64_t rows_grid = cdiv(N, trans_b ? 16 * fn : 32);
+  if (rows) {
+    if ((st = grid_ok(rows_grid, 512)) != BST_OK) return st;
+  } else {
     if ((st = plan_gemm(grouped ? G : 0, M, N, K, c == BST_F32, s, p)) != BST_OK) return st;
     if ((st = check_ws(p, ws, ws_bytes)) != BST_OK) return st;
   }
@@ -334,8 +344,7 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
   a.ckind = (uint32_t)c;
   a.cvec = vec_rows(C, ldc, 0, out_bytes(c));
   if (rows) {
-    const int fn = cdiv(N, 32) >= 2 * device_cu_count() ? 2 : 1;
-    a.grid = (uint32_t)cdiv(N, trans_b ? 16 * fn : 32);
+    a.grid = (uint32_t)rows_grid;
     const dim3 grid(a.grid), block(512);
     auto run = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, block, 0, (hipStream_t)stream, a);
@@ -485,6 +494,8 @@ bst_status bst_quant_block(bst_dtype x, int64_t M, int64_t K, int32_t block_rows
   BlockQuantArgs a{};
   bst_status st = quant_args(a, x, M, K, block_rows, ldx, ldq, lds, a.blocks);
   if (st != BST_OK) return st;
+  const int64_t squares = cdiv(M, 128) * a.kb;
+  if (block_rows == 128 && (st = grid_ok(squares, 256)) != BST_OK) return st;
   if (M == 0 || K == 0) return BST_OK;
   if (!X || !Q || !S) return set_error(BST_E_INVAL, "X, Q or S is NULL");
   if (!aligned(X, (uint64_t)out_bytes(x))) return set_error(BST_E_ALIGN, "X is not aligned to its type");
@@ -495,7 +506,7 @@ bst_status bst_quant_block(bst_dtype x, int64_t M, int64_t K, int32_t block_rows
   a.qvec = aligned(Q, 8) && ldq % 8 == 0;
   const hipStream_t s = (hipStream_t)stream;
   if (block_rows == 128) {
-    const uint32_t grid = (uint32_t)(cdiv(M, 128) * a.kb);
+    const uint32_t grid = (uint32_t)squares;
     if (x == BST_F32)
       hipLaunchKernelGGL((quant_square_kernel<X_F32>), dim3(grid), dim3(256), 0, s, a);
     else if (x == BST_BF16)

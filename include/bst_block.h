@@ -32,6 +32,9 @@
  *    call's work on the stream is done: calls that may run at the same time
  *    need a workspace each.
  *  - Every call may be captured into a graph: it only launches kernels.
+ *  - BST_E_UNSUPPORTED where a call would need more threads than a launch
+ *    holds (2^32; e.g. more than 2^23 output tiles), BST_E_INVAL where a split
+ *    output has more than 2^33 values.
  */
 #ifndef BST_BLOCK_H
 #define BST_BLOCK_H

@@ -227,3 +227,19 @@ def test_dma_scalar_operand_hazards(tu, tmp_path):
             assert m and int(m.group(1)) >= 4, (prev, cur)
             found += 1
     assert found >= 32
+
+
+def test_refuses_more_than_a_launch_holds(L):
+    big = (1 << 31) - 1
+    # 2^24 + workgroups of 256 or 512 threads
+    assert quant(L, M=1, K=big, br=128, ldx=1 << 31, ldq=1 << 31) == _lib.E_UNSUPPORTED
+    assert b"one launch" in L.bst_last_error()
+    assert gemm(L, M=big, N=16, K=16, lda=16, ldb=16, ldsa=1, ldsb=1) == _lib.E_UNSUPPORTED
+    assert gemm(L, tb=1, M=1, N=big, K=16, lda=16, ldb=16, ldsa=1, ldsb=1) == _lib.E_UNSUPPORTED
+    assert grouped(L, M=big, N=16, K=16) == _lib.E_UNSUPPORTED
+    assert grad(L, M=64, N=1 << 20, K=1 << 20, ldq=1 << 20, lds=1 << 13, lddy=1 << 20,
+                lddw=1 << 20, sched=S(tile=(128, 128), split_k=1)) == _lib.E_UNSUPPORTED
+    # the last addition counts 16-byte pieces in 31 bits
+    wide = dict(M=128, N=1 << 17, K=1 << 17, ldq=1 << 17, lds=1 << 10, sched=S(split_k=2))
+    assert grad(L, **wide) == _lib.E_INVAL
+    assert b"too large" in L.bst_last_error()
