@@ -223,7 +223,8 @@ struct BlockRowsN {
     if (wave < a.nk) fetch(wave, 0, next);
     for (uint32_t kb = wave; kb < a.nk; kb += NW) {
       const Next now = next;
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this patch has landed
+      // this patch has landed, and the other buffer's reads are done
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       if (kb + NW < a.nk) fetch(kb + NW, s ^ 1u, next);
       i32x8_t b[2];
 #pragma unroll
