@@ -342,7 +342,8 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
   a.sa_f32 = sa == BST_F32;
   a.sb_f32 = sb == BST_F32;
   a.ckind = (uint32_t)c;
-  a.cvec = vec_rows(C, ldc, 0, out_bytes(c));
+  // a tile's rows of C are stored at 31-bit offsets
+  a.cvec = vec_rows(C, ldc, 0, out_bytes(c)) && 256 * ldc * out_bytes(c) < kSpan;
   if (rows) {
     a.grid = (uint32_t)rows_grid;
     const dim3 grid(a.grid), block(512);

@@ -123,12 +123,31 @@ __device__ __forceinline__ void put_value(uint8_t* p, float v, uint32_t kind) {
     *(uint16_t*)p = (uint16_t)pack2(v, 0.0f, kind);
 }
 
+struct PutPlain {
+  uint8_t* dst;
+  template <typename V>
+  __device__ __forceinline__ void operator()(int q, V v) const {
+    ((V*)dst)[q] = v;
+  }
+};
+
+// Stores through the L2 (device-scope cache policy), at an offset into a
+// buffer of less than 2 GiB.
+struct PutThrough {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t off;
+  __device__ __forceinline__ void operator()(int q, u32x4_t v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, off + 16u * q, 0, 16);
+  }
+};
+
 // N consecutive outputs (N = 4 or 8): with `add` the addend joins in fp32
 // before the one rounding.  whole: all N are inside the row and both rows are
-// aligned for vector access; otherwise `live` of them go one by one.
-template <int N>
+// aligned for vector access; they go out through `put`.  Otherwise `live` of
+// them go one by one.
+template <int N, typename Put>
 __device__ __forceinline__ void put_run(uint8_t* dst, const uint8_t* add, float (&v)[N],
-                                        uint32_t live, bool whole, uint32_t kind) {
+                                        uint32_t live, bool whole, uint32_t kind, Put put) {
   const uint32_t es = kind == OUT_F32 ? 4u : 2u;
   if (whole) {
     if (kind == OUT_F32) {
@@ -136,7 +155,7 @@ __device__ __forceinline__ void put_run(uint8_t* dst, const uint8_t* add, float 
       for (int q = 0; q < N / 4; ++q) {
         f32x4_t o = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
         if (add != nullptr) o += ((const f32x4_t*)add)[q];
-        ((f32x4_t*)dst)[q] = o;
+        put(q, __builtin_bit_cast(u32x4_t, o));
       }
     } else {
       uint32_t a[N / 2], o[N / 2];
@@ -157,9 +176,9 @@ __device__ __forceinline__ void put_run(uint8_t* dst, const uint8_t* add, float 
 #pragma unroll
       for (int e = 0; e < N / 2; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1], kind);
       if constexpr (N == 8)
-        *(u32x4_t*)dst = u32x4_t{o[0], o[1], o[2], o[3]};
+        put(0, u32x4_t{o[0], o[1], o[2], o[3]});
       else
-        *(u32x2_t*)dst = u32x2_t{o[0], o[1]};
+        put(0, u32x2_t{o[0], o[1]});
     }
     return;
   }
@@ -167,6 +186,12 @@ __device__ __forceinline__ void put_run(uint8_t* dst, const uint8_t* add, float 
   for (int e = 0; e < N; ++e)
     if ((uint32_t)e < live)
       put_value(dst + e * es, v[e] + (add != nullptr ? out_value(add + e * es, kind) : 0.0f), kind);
+}
+
+template <int N>
+__device__ __forceinline__ void put_run(uint8_t* dst, const uint8_t* add, float (&v)[N],
+                                        uint32_t live, bool whole, uint32_t kind) {
+  put_run(dst, add, v, live, whole, kind, PutPlain{dst});
 }
 
 // Where a tile goes: the final matrix, or a slice's partial sums (fp32, rows
@@ -192,7 +217,14 @@ struct Strip {
   static constexpr int BYTES = 32 * PITCH * 4;
 };
 
-template <int FM, int FN>
+// THROUGH: whole runs go through the L2 to memory, so that they do not stay
+// dirty in it, take the place of operand panels and wait for the write-back at
+// the kernel's end: 8192 rows over 8 groups of 4096 x 2048 99.9 -> 95.5 us,
+// 8192 x 8192 x 4096 272 -> 265, 1024 x 2048 x 4096 19.7 -> 19.4.  Not for what
+// the next launch reads or what was read into the L2 just before (partial
+// sums; a gradient with an addend: 265 -> 278 us at 8192 x 4096 x 4096).  It
+// needs a tile whose rows span less than 2 GiB.
+template <bool THROUGH, int FM, int FN>
 __device__ __forceinline__ void store_wave_tile(lds_t* strip, f32x16_t (&acc)[FM][FN], uint32_t m0,
                                                 uint32_t n0, const OutTile& o) {
   constexpr int TN = FN * 32, P = Strip<TN>::PITCH;
@@ -201,6 +233,8 @@ __device__ __forceinline__ void store_wave_tile(lds_t* strip, f32x16_t (&acc)[FM
   typedef __attribute__((address_space(3))) f32x4_t lds_f4_t;
   const uint32_t lane = threadIdx.x & 63u, r = lane & 31u, hi = lane >> 5;
   const uint32_t es = o.kind == OUT_F32 ? 4u : 2u;
+  const __amdgpu_buffer_rsrc_t through =
+      __builtin_amdgcn_make_buffer_rsrc(o.dst, (short)0, (int)0x7fffffff, 0x00020000);
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     if (m0 + i * 32 >= o.rows) return;  // wave-uniform
@@ -222,7 +256,12 @@ __device__ __forceinline__ void store_wave_tile(lds_t* strip, f32x16_t (&acc)[FM
       if (m < o.rows && n < o.cols) {
         uint8_t* d = o.dst + (int64_t)m * o.ld_bytes + (int64_t)n * es;
         const uint8_t* ad = o.add ? o.add + (int64_t)m * o.ldadd_bytes + (int64_t)n * es : nullptr;
-        put_run<8>(d, ad, v, o.cols - n, o.vec && o.cols - n >= 8u, o.kind);
+        const bool whole = o.vec && o.cols - n >= 8u;
+        if constexpr (THROUGH)
+          put_run(d, ad, v, o.cols - n, whole, o.kind,
+                  PutThrough{through, m * (uint32_t)o.ld_bytes + n * es});
+        else
+          put_run(d, ad, v, o.cols - n, whole, o.kind, PutPlain{d});
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

@@ -661,7 +661,11 @@ struct BlockGemm {
       o.ld_bytes = a.ldc * es;
       o.dst = a.C + (arow * a.ldc + n0) * es;
     }
-    store_wave_tile<FM, FN>(lds() + wave * Strip<TN>::BYTES, acc, wm * TM, wn * TN, o);
+    lds_t* const strip = lds() + wave * Strip<TN>::BYTES;
+    if (!GROUPED && a.part != nullptr)
+      store_wave_tile<false>(strip, acc, wm * TM, wn * TN, o);
+    else
+      store_wave_tile<true>(strip, acc, wm * TM, wn * TN, o);
   }
 };
 

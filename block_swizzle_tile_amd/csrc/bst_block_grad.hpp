@@ -323,7 +323,7 @@ struct BlockGrad {
         o.add = a.add + (g * a.strideadd + (int64_t)k0 * a.ldadd + n0) * es;
       }
     }
-    store_wave_tile<FM, FN>(lds() + wave * Strip<TN>::BYTES, acc, wm * TM, wn * TN, o);
+    store_wave_tile<false>(lds() + wave * Strip<TN>::BYTES, acc, wm * TM, wn * TN, o);
   }
 };
 
