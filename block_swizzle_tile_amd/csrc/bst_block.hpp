@@ -123,31 +123,12 @@ __device__ __forceinline__ void put_value(uint8_t* p, float v, uint32_t kind) {
     *(uint16_t*)p = (uint16_t)pack2(v, 0.0f, kind);
 }
 
-struct PutPlain {
-  uint8_t* dst;
-  template <typename V>
-  __device__ __forceinline__ void operator()(int q, V v) const {
-    ((V*)dst)[q] = v;
-  }
-};
-
-// Stores through the L2 (device-scope cache policy), at an offset into a
-// buffer of less than 2 GiB.
-struct PutThrough {
-  __amdgpu_buffer_rsrc_t r;
-  uint32_t off;
-  __device__ __forceinline__ void operator()(int q, u32x4_t v) const {
-    __builtin_amdgcn_raw_buffer_store_b128(v, r, off + 16u * q, 0, 16);
-  }
-};
-
 // N consecutive outputs (N = 4 or 8): with `add` the addend joins in fp32
 // before the one rounding.  whole: all N are inside the row and both rows are
-// aligned for vector access; they go out through `put`.  Otherwise `live` of
-// them go one by one.
-template <int N, typename Put>
+// aligned for vector access; otherwise `live` of them go one by one.
+template <int N>
 __device__ __forceinline__ void put_run(uint8_t* dst, const uint8_t* add, float (&v)[N],
-                                        uint32_t live, bool whole, uint32_t kind, Put put) {
+                                        uint32_t live, bool whole, uint32_t kind) {
   const uint32_t es = kind == OUT_F32 ? 4u : 2u;
   if (whole) {
     if (kind == OUT_F32) {
@@ -155,7 +136,7 @@ __device__ __forceinline__ void put_run(uint8_t* dst, const uint8_t* add, float 
       for (int q = 0; q < N / 4; ++q) {
         f32x4_t o = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
         if (add != nullptr) o += ((const f32x4_t*)add)[q];
-        put(q, __builtin_bit_cast(u32x4_t, o));
+        ((f32x4_t*)dst)[q] = o;
       }
     } else {
       uint32_t a[N / 2], o[N / 2];
@@ -176,9 +157,9 @@ __device__ __forceinline__ void put_run(uint8_t* dst, const uint8_t* add, float 
 #pragma unroll
       for (int e = 0; e < N / 2; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1], kind);
       if constexpr (N == 8)
-        put(0, u32x4_t{o[0], o[1], o[2], o[3]});
+        *(u32x4_t*)dst = u32x4_t{o[0], o[1], o[2], o[3]};
       else
-        put(0, u32x2_t{o[0], o[1]});
+        *(u32x2_t*)dst = u32x2_t{o[0], o[1]};
     }
     return;
   }
@@ -186,12 +167,6 @@ __device__ __forceinline__ void put_run(uint8_t* dst, const uint8_t* add, float 
   for (int e = 0; e < N; ++e)
     if ((uint32_t)e < live)
       put_value(dst + e * es, v[e] + (add != nullptr ? out_value(add + e * es, kind) : 0.0f), kind);
-}
-
-template <int N>
-__device__ __forceinline__ void put_run(uint8_t* dst, const uint8_t* add, float (&v)[N],
-                                        uint32_t live, bool whole, uint32_t kind) {
-  put_run(dst, add, v, live, whole, kind, PutPlain{dst});
 }
 
 // Where a tile goes: the final matrix, or a slice's partial sums (fp32, rows
@@ -206,17 +181,16 @@ struct OutTile {
 };
 
 // Stores a wave's TM x TN sub-tile held as 32x32 accumulators (lane l: row
-// l & 31 of the fragment, columns 8q + 4(l >> 5) + 0..3), one 32-row strip at
-// a time through the wave's own LDS strip, so that global stores are runs of
-// a row.  Waves do not wait for each other: LDS accesses of one wave complete
-// in order.  Strip rows are padded by 4 floats: the 32 rows' quads then fall
-// on different banks.
-template <int TN>
-struct Strip {
-  static constexpr int PITCH = TN + 4;  // floats
-  static constexpr int BYTES = 32 * PITCH * 4;
-};
-
+// l & 31 of the fragment, columns 8q + 4(l >> 5) + 0..3), one strip of 32 rows
+// at a time through the wave's own LDS, so that global stores are runs of a
+// row.  Waves do not wait for each other: LDS accesses of one wave complete in
+// order.  Whole rows of vectors have two forms of their own, because nothing
+// hides a tile's epilogue: 16-bit outputs are packed before they go through
+// LDS, 32-bit ones are not.  One unrolled form for all was slower by its own
+// code and waits (one 256x256 tile per workgroup, 16 of them, K = 128: 9.6 us
+// against 6.7; 8192 rows over 8 groups of 4096 x 2048: 95 against 91), and so
+// were 16-bit strips of 128 rows (92).
+//
 // THROUGH: whole runs go through the L2 to memory, so that they do not stay
 // dirty in it, take the place of operand panels and wait for the write-back at
 // the kernel's end: 8192 rows over 8 groups of 4096 x 2048 99.9 -> 95.5 us,
@@ -224,49 +198,128 @@ struct Strip {
 // the next launch reads or what was read into the L2 just before (partial
 // sums; a gradient with an addend: 265 -> 278 us at 8192 x 4096 x 4096).  It
 // needs a tile whose rows span less than 2 GiB.
-template <bool THROUGH, int FM, int FN>
-__device__ __forceinline__ void store_wave_tile(lds_t* strip, f32x16_t (&acc)[FM][FN], uint32_t m0,
-                                                uint32_t n0, const OutTile& o) {
-  constexpr int TN = FN * 32, P = Strip<TN>::PITCH;
-  constexpr int CPR = TN / 8;        // runs of 8 columns per row
-  constexpr int RPI = 64 / CPR;      // rows one pass of the wave stores
+template <int FM, int FN>
+struct Strips {
+  static constexpr int TN = FN * 32;
+  // 32-bit strips: rows are padded by 4 floats, so that the 32 rows' quads fall
+  // on different banks
+  static constexpr int PITCH = TN + 4;
+  static constexpr int BYTES = 32 * PITCH * 4;
+  static constexpr int CPR = TN / 8;    // runs of 8 columns per row
+  static constexpr int RPI = 64 / CPR;  // rows one pass of the wave stores
   typedef __attribute__((address_space(3))) f32x4_t lds_f4_t;
-  const uint32_t lane = threadIdx.x & 63u, r = lane & 31u, hi = lane >> 5;
-  const uint32_t es = o.kind == OUT_F32 ? 4u : 2u;
-  const __amdgpu_buffer_rsrc_t through =
-      __builtin_amdgcn_make_buffer_rsrc(o.dst, (short)0, (int)0x7fffffff, 0x00020000);
+
+  // 16-bit rows of TN * 2 bytes; their 16-byte chunks are XORed by the row, so
+  // that 8 rows' chunks (write) and a row's chunks (read) fall on different banks
+  static __device__ __forceinline__ uint32_t at16(uint32_t row, uint32_t ch) {
+    return row * (TN * 2) + ((ch ^ (CPR == 8 ? row & 7u : (row >> 1) & 3u)) << 4);
+  }
+  template <uint32_t KIND>
+  static __device__ __forceinline__ void strip16(lds_t* s, const f32x16_t (&acc)[FN]) {
+    const uint32_t lane = threadIdx.x & 63u, r = lane & 31u, hi = lane >> 5;
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    if (m0 + i * 32 >= o.rows) return;  // wave-uniform
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        // quads q and q + 1 of a row are in lanes l and l + 32: after the swaps
+        // lane l holds all 8 columns of q, and l + 32 those of q + 1
+        u32x2_t v[2];
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const uint32_t x = pack2(acc[j][4 * q + 2 * d], acc[j][4 * q + 2 * d + 1], KIND);
+          const uint32_t y = pack2(acc[j][4 * q + 4 + 2 * d], acc[j][4 * q + 5 + 2 * d], KIND);
+          const auto w = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+          v[d] = u32x2_t{w[0], w[1]};
+        }
+        *(lds_u32x4_t*)(s + at16(r, j * 4 + q + hi)) = u32x4_t{v[0][0], v[1][0], v[0][1], v[1][1]};
+      }
+  }
+  static __device__ __forceinline__ void strip32(lds_t* s, const f32x16_t (&acc)[FN]) {
+    const uint32_t lane = threadIdx.x & 63u, r = lane & 31u, hi = lane >> 5;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        *(lds_f4_t*)(strip + (r * P + j * 32 + 8 * q + 4 * hi) * 4) =
-            f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                    acc[i][j][4 * q + 3]};
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        *(lds_f4_t*)(s + (r * PITCH + j * 32 + 8 * q + 4 * hi) * 4) =
+            f32x4_t{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+  }
+  static __device__ __forceinline__ void written() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+  template <bool THROUGH>
+  static __device__ __forceinline__ void store(lds_t* s, f32x16_t (&acc)[FM][FN], uint32_t m0,
+                                               uint32_t n0, const OutTile& o) {
+    if (m0 >= o.rows || n0 >= o.cols) return;  // wave-uniform, as all branches but the last
+    const uint32_t lane = threadIdx.x & 63u, row = lane / CPR, c = (lane % CPR) * 8;
+    const uint32_t n = n0 + c;
+    const bool runs = o.vec && o.cols % 8 == 0;
+    const __amdgpu_buffer_rsrc_t through =
+        __builtin_amdgcn_make_buffer_rsrc(o.dst, (short)0, (int)0x7fffffff, 0x00020000);
+    auto put = [&](uint32_t m, uint32_t off, u32x4_t v) {  // 16 bytes, off bytes into row m
+      if constexpr (THROUGH)
+        __builtin_amdgcn_raw_buffer_store_b128(v, through, m * (uint32_t)o.ld_bytes + off, 0, 16);
+      else
+        *(u32x4_t*)(o.dst + (int64_t)m * o.ld_bytes + off) = v;
+    };
+    if (runs && o.kind != OUT_F32 && o.add == nullptr) {
 #pragma unroll
-    for (int s = 0; s < 32 / RPI; ++s) {
-      const uint32_t row = s * RPI + lane / CPR, c = (lane % CPR) * 8;
-      const f32x4_t a = *(const lds_f4_t*)(strip + (row * P + c) * 4);
-      const f32x4_t b = *(const lds_f4_t*)(strip + (row * P + c + 4) * 4);
-      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      const uint32_t m = m0 + i * 32 + row, n = n0 + c;
-      if (m < o.rows && n < o.cols) {
-        uint8_t* d = o.dst + (int64_t)m * o.ld_bytes + (int64_t)n * es;
-        const uint8_t* ad = o.add ? o.add + (int64_t)m * o.ldadd_bytes + (int64_t)n * es : nullptr;
-        const bool whole = o.vec && o.cols - n >= 8u;
-        if constexpr (THROUGH)
-          put_run(d, ad, v, o.cols - n, whole, o.kind,
-                  PutThrough{through, m * (uint32_t)o.ld_bytes + n * es});
-        else
-          put_run(d, ad, v, o.cols - n, whole, o.kind, PutPlain{d});
+      for (int i = 0; i < FM; ++i) {
+        if (o.kind == OUT_BF16) strip16<OUT_BF16>(s, acc[i]);
+        else strip16<OUT_F16>(s, acc[i]);
+        written();
+#pragma unroll
+        for (int p = 0; p < 32 / RPI; ++p) {
+          const uint32_t r = p * RPI + row, m = m0 + i * 32 + r;
+          const u32x4_t v = *(const lds_u32x4_t*)(s + at16(r, lane % CPR));
+          if (m < o.rows && n < o.cols) put(m, n * 2, v);
+        }
+        written();
+      }
+    } else if (runs && o.kind == OUT_F32) {
+      constexpr int P = 32 / RPI;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        strip32(s, acc[i]);
+        written();
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const uint32_t r = p * RPI + row, m = m0 + i * 32 + r;
+          f32x4_t x = *(const lds_f4_t*)(s + (r * PITCH + c) * 4);
+          f32x4_t y = *(const lds_f4_t*)(s + (r * PITCH + c + 4) * 4);
+          if (m < o.rows && n < o.cols) {
+            if (o.add != nullptr) {
+              const f32x4_t* a = (const f32x4_t*)(o.add + (int64_t)m * o.ldadd_bytes + n * 4);
+              x += a[0];
+              y += a[1];
+            }
+            put(m, n * 4, __builtin_bit_cast(u32x4_t, x));
+            put(m, n * 4 + 16, __builtin_bit_cast(u32x4_t, y));
+          }
+        }
+        written();
+      }
+    } else {
+      const uint32_t es = o.kind == OUT_F32 ? 4u : 2u;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        strip32(s, acc[i]);
+        written();
+#pragma unroll 1
+        for (uint32_t r = row; r < 32; r += RPI) {
+          const uint32_t m = m0 + i * 32 + r;
+          const f32x4_t x = *(const lds_f4_t*)(s + (r * PITCH + c) * 4);
+          const f32x4_t y = *(const lds_f4_t*)(s + (r * PITCH + c + 4) * 4);
+          float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+          if (m < o.rows && n < o.cols) {
+            uint8_t* d = o.dst + (int64_t)m * o.ld_bytes + (int64_t)n * es;
+            const uint8_t* ad = o.add ? o.add + (int64_t)m * o.ldadd_bytes + (int64_t)n * es : nullptr;
+            put_run<8>(d, ad, v, o.cols - n, o.vec && o.cols - n >= 8u, o.kind);
+          }
+        }
+        written();
       }
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
-}
+};
 
 // Sum of the split partials in slice order, the addend, and the one rounding.
 // part: [split][count][rows][pitch] fp32, pitch a multiple of 4.

@@ -88,7 +88,7 @@ struct BlockGemm {
   static_assert(SA_N < NW, "one scale instruction per wave");
   static_assert(RING || MODE != MODE_EXACT, "the two-stage loop has no exact form");
   static_assert(TM % 32 == 0 && TN % 32 == 0 && 128 % TN == 0, "wave tile");
-  static_assert(NW * Strip<TN>::BYTES <= LDS_BYTES, "the epilogue's strips fit");
+  static_assert(NW * Strips<FM, FN>::BYTES <= LDS_BYTES, "the epilogue's strips fit");
   static_assert((STAGES - 1) * LPS < 64, "vmcnt holds 6 bits");
   static_assert(LDS_BYTES + (GROUPED ? (int)sizeof(RowGroups) : 0) <= 160 * 1024, "LDS budget");
 
@@ -661,11 +661,12 @@ struct BlockGemm {
       o.ld_bytes = a.ldc * es;
       o.dst = a.C + (arow * a.ldc + n0) * es;
     }
-    lds_t* const strip = lds() + wave * Strip<TN>::BYTES;
+    using S = Strips<FM, FN>;
+    lds_t* const strips = lds() + wave * S::BYTES;
     if (!GROUPED && a.part != nullptr)
-      store_wave_tile<false>(strip, acc, wm * TM, wn * TN, o);
+      S::template store<false>(strips, acc, wm * TM, wn * TN, o);
     else
-      store_wave_tile<true>(strip, acc, wm * TM, wn * TN, o);
+      S::template store<true>(strips, acc, wm * TM, wn * TN, o);
   }
 };
 

@@ -80,7 +80,7 @@ struct BlockGrad {
 
   static_assert(D * XCH % NT == 0 && D * YCH % NT == 0, "whole loads");
   static_assert(2 * STAGE_BYTES + (int)sizeof(RowGroups) <= 160 * 1024, "LDS budget");
-  static_assert(NW * Strip<TN>::BYTES <= 2 * STAGE_BYTES, "the epilogue's strips fit");
+  static_assert(NW * Strips<FM, FN>::BYTES <= 2 * STAGE_BYTES, "the epilogue's strips fit");
 
   static __device__ __forceinline__ lds_t* lds() {
     __shared__ __attribute__((aligned(16))) uint8_t buf[2 * STAGE_BYTES];
@@ -323,7 +323,8 @@ struct BlockGrad {
         o.add = a.add + (g * a.strideadd + (int64_t)k0 * a.ldadd + n0) * es;
       }
     }
-    store_wave_tile<false>(lds() + wave * Strip<TN>::BYTES, acc, wm * TM, wn * TN, o);
+    Strips<FM, FN>::template store<false>(lds() + wave * Strips<FM, FN>::BYTES, acc, wm * TM,
+                                          wn * TN, o);
   }
 };
 
