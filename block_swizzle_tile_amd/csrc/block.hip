@@ -396,7 +396,7 @@ bst_status grad(bst_dtype dy, bst_dtype dw, bool grouped, int32_t G, const int32
                      (long long)stridedw, (long long)((K - 1) * lddw + N));
   if (grouped && add && strideadd < 0) return set_error(BST_E_INVAL, "negative strideadd");
   if (M > 0) {
-    if ((st = codes_ok("Q", Q, ldq, K, 1)) != BST_OK) return st;
+    if ((st = codes_ok("Q", Q, ldq, K, 64)) != BST_OK) return st;
     if ((st = scales_ok("S", S, BST_E8M0, lds, cdiv(K, 128))) != BST_OK) return st;
     if ((st = matrix_ok("dY", dY, lddy, N, out_bytes(dy))) != BST_OK) return st;
   }
@@ -438,7 +438,8 @@ bst_status grad(bst_dtype dy, bst_dtype dw, bool grouped, int32_t G, const int32
   a.dwkind = (uint32_t)dw;
   a.dwvec = vec_rows(dW, lddw, n > 1 ? stridedw : 0, es) &&
             (!add || vec_rows(add, ldadd, n > 1 ? strideadd : 0, es));
-  a.dyvec = vec_rows(dY, lddy, 0, out_bytes(dy));
+  // a stage's 64 rows are loaded at 31-bit offsets
+  a.dyvec = vec_rows(dY, lddy, 0, out_bytes(dy)) && 64 * lddy * out_bytes(dy) < kSpan;
   a.mc = make_map_consts((uint32_t)cdiv(K, p.tm), (uint32_t)cdiv(N, p.tn), s.off, s.dir,
                          (uint32_t)p.tiles, 1u);
   if (p.split > 1) {

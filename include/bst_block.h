@@ -143,6 +143,7 @@ bst_status bst_grouped_gemm_block_scaled(bst_dtype c, int32_t trans_b, int32_t G
  *   tile_m x tile_n of sched: 128x128 or 256x256 (tile_m along K, tile_k 0);
  *   the other fields as for bst_gemm_block_scaled, split_k along M.
  *   ws: bst_block_workspace_bytes(1, ...) bytes.
+ *   BST_E_UNSUPPORTED if 64 rows of Q span 2 GiB.
  */
 bst_status bst_weight_grad(bst_dtype dy, bst_dtype dw, int64_t M, int64_t N, int64_t K,
                            const uint8_t* Q_dev, int64_t ldq, const uint8_t* S_dev, int64_t lds,
