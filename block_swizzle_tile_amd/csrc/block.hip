@@ -219,17 +219,23 @@ bst_status plan_grad(int64_t count, int64_t M, int64_t N, int64_t K, const Sched
 
 // Products that the kernels for a few rows take, if no tile and no split is
 // asked for.  They need one launch and no partial sums, but a workgroup walks
-// all of K, so they lose to a split where K is long or the rows fill more
-// operands.  Weights N x K: 16 rows 7.1 us against 10.3 (4096 x 4096), 18.5
-// against 16.2 at K = 14336; 32 rows 9.9 against 10.3 and 27.7 against 17.
-// Weights K x N: one row 7.0 us against 9.2 (4096 x 4096) and 9.6 against 10.5 at
-// K = 8192; 33 rows 7.0 against 10.6 at K = 2056 and 11.4 against 11.7 at 4096;
-// and from 16384 columns on the tiles fill the chip unsplit.
+// all of K and reads all of A, so they lose to a split where K is long or the
+// rows are many, and to unsplit tiles where the columns are many.  Times in us,
+// these kernels against the tiles, M x N x K:
+// N x K weights: 1 x 4096 x 4096 5.2 / 9.2, 1 x 4096 x 14336 12.8 / 14.6,
+//   16 x 4096 x 6144 8.9 / 9.9, 16 x 4096 x 8192 12.2 / 10.5,
+//   32 x 4096 x 2944 7.3 / 9.9, 32 x 4096 x 4096 10.6 / 10.0,
+//   1 x 1024 x 8192 7.6 / 8.1, 1 x 2048 x 14336 11.6 / 10.0 (the one loss of
+//   the rule), 1 x 16384 x 4096 16.0 / 14.8;
+// K x N weights: 1 x 4096 x 4096 7.2 / 7.9, 1 x 4096 x 8192 14.1 / 9.8,
+//   32 x 8192 x 2048 6.9 / 9.9, 33 x 4112 x 2056 6.8 / 9.7,
+//   33 x 4096 x 4096 11.7 / 10.5, 1 x 14336 x 2048 10.6 / 8.9.
 bool takes_rows(int32_t trans_b, int64_t M, int64_t N, int64_t K, const Sched& s) {
   if (s.tm != 0 || s.tn != 0 || s.split != 0) return false;
-  const int64_t nk = cdiv(K, 128);
-  if (trans_b) return M <= 16 || (M <= 32 && nk <= 32);
-  return M <= 64 && cdiv(nk, 8) * cdiv(M, 32) <= 8 && cdiv(N, 128) * 2 < device_cu_count();
+  const int64_t nk = cdiv(K, 128), cus = device_cu_count();
+  if (trans_b)
+    return M <= 32 && M * nk <= 768 && cdiv(N, 128) * 2 < cus;
+  return M <= 64 && nk <= (M <= 32 ? 32 : 24) && cdiv(N, 32) <= cus;
 }
 
 bst_status check_ws(const Plan& p, const void* ws, size_t bytes) {
@@ -297,11 +303,7 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
   }
   const bool rows = !grouped && takes_rows(trans_b, M, N, K, s);
   Plan p;
-  const int fn = cdiv(N, 32) >= 2 * device_cu_count() ? 2 : 1;  // a rows kernel's operands of B
-  const int64_t rows_grid = cdiv(N, trans_b ? 16 * fn : 32);
-  if (rows) {
-    if ((st = grid_ok(rows_grid, 512)) != BST_OK) return st;
-  } else {
+  if (!rows) {
     if ((st = plan_gemm(grouped ? G : 0, M, N, K, c == BST_F32, s, p)) != BST_OK) return st;
     if ((st = check_ws(p, ws, ws_bytes)) != BST_OK) return st;
   }
@@ -345,7 +347,7 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
   // a tile's rows of C are stored at 31-bit offsets
   a.cvec = vec_rows(C, ldc, 0, out_bytes(c)) && 256 * ldc * out_bytes(c) < kSpan;
   if (rows) {
-    a.grid = (uint32_t)rows_grid;
+    a.grid = (uint32_t)cdiv(N, trans_b ? 16 : 32);
     const dim3 grid(a.grid), block(512);
     auto run = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, block, 0, (hipStream_t)stream, a);
@@ -356,12 +358,8 @@ bst_status gemm(bst_dtype c, int32_t trans_b, bool grouped, int32_t G, const int
       if (M <= 32) return exact ? run(block_rows_n_kernel<1, true>) : run(block_rows_n_kernel<1, false>);
       return exact ? run(block_rows_n_kernel<2, true>) : run(block_rows_n_kernel<2, false>);
     }
-    if (fn == 2) {
-      if (M <= 16) return exact ? run(block_rows_kernel<1, 2, true>) : run(block_rows_kernel<1, 2, false>);
-      return exact ? run(block_rows_kernel<2, 2, true>) : run(block_rows_kernel<2, 2, false>);
-    }
-    if (M <= 16) return exact ? run(block_rows_kernel<1, 1, true>) : run(block_rows_kernel<1, 1, false>);
-    return exact ? run(block_rows_kernel<2, 1, true>) : run(block_rows_kernel<2, 1, false>);
+    if (M <= 16) return exact ? run(block_rows_kernel<1, true>) : run(block_rows_kernel<1, false>);
+    return exact ? run(block_rows_kernel<2, true>) : run(block_rows_kernel<2, false>);
   }
   if (p.split > 1) {
     a.part = static_cast<float*>(ws);

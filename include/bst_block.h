@@ -90,7 +90,7 @@ bst_status bst_dequant_block(bst_dtype x, int64_t M, int64_t K, int32_t block_ro
  *   an fp32 output is computed on bf16 instructions from the same codes,
  *   which keep fp32 throughout, and takes up to twice as long.
  *   A few rows of A (at most 32, or 64 with trans_b = 0) run on kernels of
- *   their own where K is not too long and no tile or split is asked for; they
+ *   their own where K and N are not too long and no tile or split is asked for; they
  *   read every weight once, in one launch and without a workspace.
  *   sched: NULL, or a schedule of which tile_m x tile_n (0 x 0 = chosen by
  *   the sizes; 32x128, 64x128, 128x128, and 256x256 for 16-bit outputs), swizzle_offset,
