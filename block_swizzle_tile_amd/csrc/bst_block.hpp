@@ -26,9 +26,11 @@ __device__ __forceinline__ float e8m0_value(uint32_t e) {
 
 // Groups of stacked rows, in LDS: each group's first row, its first task among
 // the full tile-rows, and its first tile-row among the partial ones (a group
-// has at most one), with the totals behind the last group.  The partial tiles
-// come after all full ones: they are the shorter tasks, and workgroups start
-// in order, so the chip's last round is filled with them.
+// has at most one; those of more than half a tile's rows are counted in the low
+// 16 bits, the others in the high ones), with the totals behind the last group.
+// Partial tiles come after all full ones, and the smaller ones last: they are
+// the shorter tasks, and workgroups start in order, so the chip's last round
+// is filled with them.
 struct RowGroups {
   uint32_t first_row[kMaxGroups + 1];
   uint32_t first_task[kMaxGroups + 1];
@@ -60,7 +62,8 @@ __device__ inline void build_row_groups(RowGroups& t, const int32_t* group_m, ui
       t.first_task[g] = tasks;
       t.first_tail[g] = tails;
       tasks += (hi - lo) / bm * loops_n;
-      tails += (hi - lo) % bm != 0 ? 1u : 0u;
+      const uint32_t rest = (hi - lo) % bm;
+      tails += rest > bm / 2 ? 1u : rest != 0 ? 0x10000u : 0u;
       if (g + 1 == G) t.first_row[G] = hi;
     }
     uint32_t ts = tasks, ls = tails;
@@ -85,11 +88,12 @@ __device__ inline void build_row_groups(RowGroups& t, const int32_t* group_m, ui
 
 // The last group whose first entry is at most x (groups without entries of
 // their own share the next one's).
+template <int SHIFT = 0, uint32_t MASK = 0xffffffffu>
 __device__ __forceinline__ uint32_t find_group(const uint32_t* first, uint32_t G, uint32_t x) {
   uint32_t lo = 0, hi = G - 1;
   while (lo < hi) {
     const uint32_t mid = (lo + hi + 1) >> 1;
-    if (first[mid] <= x) lo = mid; else hi = mid - 1;
+    if ((first[mid] >> SHIFT & MASK) <= x) lo = mid; else hi = mid - 1;
   }
   return __builtin_amdgcn_readfirstlane(lo);
 }

@@ -529,8 +529,9 @@ struct BlockGemm {
       const uint32_t loops_n = (a.N + BN - 1) / BN;
       build_row_groups(groups, a.group_m, a.G, a.M, BM, loops_n);
       const uint32_t full = __builtin_amdgcn_readfirstlane(groups.first_task[a.G]);
-      const uint32_t tails = __builtin_amdgcn_readfirstlane(groups.first_tail[a.G]) * loops_n;
-      if (blockIdx.x >= full + tails) return;  // the whole workgroup
+      const uint32_t tails = __builtin_amdgcn_readfirstlane(groups.first_tail[a.G]);
+      const uint32_t large = tails & 0xffffu;
+      if (blockIdx.x >= full + (large + (tails >> 16)) * loops_n) return;  // the whole workgroup
       if (blockIdx.x < full) {
         const uint32_t u = logical_wg(a.remap, full);
         g = find_group(groups.first_task, a.G, u);
@@ -540,7 +541,9 @@ struct BlockGemm {
         t.n = __builtin_amdgcn_readfirstlane(t.n);
       } else {
         const uint32_t v = blockIdx.x - full;
-        g = find_group(groups.first_tail, a.G, v / loops_n);
+        const uint32_t r = v / loops_n;
+        g = r < large ? find_group<0, 0xffffu>(groups.first_tail, a.G, r)
+                      : find_group<16, 0xffffu>(groups.first_tail, a.G, r - large);
         t.m = __builtin_amdgcn_readfirstlane((groups.first_row[g + 1] - groups.first_row[g]) / BM);
         t.n = v % loops_n;
       }
