@@ -181,39 +181,41 @@ bst_status plan_gemm(int64_t count, int64_t M, int64_t N, int64_t K, bool exact,
   return plan_workspace(p, M, N);
 }
 
-// Tile and split (along the rows) of a weight gradient.
-bst_status plan_grad(int64_t count, int64_t M, int64_t N, int64_t K, const Sched& s, Plan& p) {
+// Tile and split (along the rows) of a weight gradient; parts: bf16 parts of dY
+// (1 to 3).  What is not asked for is the pair of least cost, in microseconds,
+// of a model with three terms: a stage of 64 rows takes as long as the table
+// says (one workgroup per CU; two take twice as long), a slice's partial sums
+// are written and read once at 5 TB/s, and adding them is one launch more.
+// Against the best of both tiles and splits 1 to 32 the choice is within 10%
+// over 64 .. 8192 rows and weights from 64 x 64 to 4096 x 4096 in 16 of 17
+// shapes (16384 rows, 1024 x 1024: 61.0 us against 52.8); the types' own costs
+// matter with fp16 and fp32 gradients (4096 rows, 2048 x 2048: fp32 171 us on
+// 128x128 unsplit, 130 on 256x256 cut four ways; fp16 129 and 99).
+bst_status plan_grad(int64_t count, int64_t M, int64_t N, int64_t K, int parts, const Sched& s,
+                     Plan& p) {
+  static constexpr double kStage[3][2] = {{0.75, 1.75}, {1.95, 4.7}, {2.6, 6.2}};
   const int64_t cus = device_cu_count(), G = std::max<int64_t>(count, 1);
-  p.tm = s.tm;
-  p.tn = s.tn;
-  if (p.tm == 0 && p.tn == 0) {
-    const int64_t large = G * cdiv(K, 256) * cdiv(N, 256);
-    p.tm = p.tn = large * 4 >= cus * 3 ? 256 : 128;
-  }
-  if (!(p.tm == p.tn && (p.tm == 128 || p.tm == 256)))
-    return set_error(BST_E_UNSUPPORTED, "no weight-gradient kernel with tile %ux%u", p.tm, p.tn);
-  p.tiles = G * cdiv(K, p.tm) * cdiv(N, p.tn);
-  const int64_t stages = cdiv(cdiv(M, G), 64);
-  int64_t split = s.split;
-  if (split == 0) {
-    // The split of least cost, in microseconds: a stage of 64 rows is about
-    // 1.5 (2 on the large tile), a slice's partial sums are written and read
-    // once at 5 TB/s, and adding them is one launch more.  Against the best of
-    // splits 1 to 32 this is within 10% over 64 .. 8192 rows and weights from
-    // 64 x 64 to 4096 x 4096.
-    const double stage = p.tm == 128 ? 1.5 : 2.0, slice = (double)G * K * N * 8 / 5e6;
-    const int64_t at_once = p.tm == 128 ? 2 * cus : cus;
-    double best = 0;
-    for (int64_t n = 1; n <= std::min<int64_t>(32, std::max<int64_t>(stages, 1)); ++n) {
-      const double cost = cdiv(p.tiles * n, at_once) * cdiv(stages, n) * stage +
+  if (!(s.tm == s.tn && (s.tm == 0 || s.tm == 128 || s.tm == 256)))
+    return set_error(BST_E_UNSUPPORTED, "no weight-gradient kernel with tile %ux%u", s.tm, s.tn);
+  const int64_t stages = std::max<int64_t>(cdiv(cdiv(M, G), 64), 1);
+  const double slice = (double)G * K * N * 8 / 5e6 + 0.07;
+  double best = -1;
+  for (int64_t tile = 128; tile <= 256; tile += 128) {
+    if (s.tm != 0 && s.tm != tile) continue;
+    const int64_t tiles = G * cdiv(K, tile) * cdiv(N, tile);
+    const double stage = kStage[parts - 1][tile / 256];
+    for (int64_t n = 1; n <= std::min<int64_t>(s.split ? s.split : 32, stages); ++n) {
+      if (s.split && n != std::min<int64_t>(s.split, stages)) continue;
+      const double cost = (double)cdiv(tiles * n, cus) * cdiv(stages, n) * stage +
                           (n > 1 ? n * slice + 2 : 0);
-      if (split == 0 || cost < best) {
-        split = n;
+      if (best < 0 || cost < best) {
         best = cost;
+        p.tm = p.tn = (uint32_t)tile;
+        p.tiles = tiles;
+        p.split = (uint32_t)n;
       }
     }
   }
-  p.split = (uint32_t)std::max<int64_t>(1, std::min<int64_t>(split, std::max<int64_t>(stages, 1)));
   return plan_workspace(p, G * K, N);
 }
 
@@ -399,9 +401,9 @@ bst_status grad(bst_dtype dy, bst_dtype dw, bool grouped, int32_t G, const int32
     if ((st = matrix_ok("dY", dY, lddy, N, out_bytes(dy))) != BST_OK) return st;
   }
   Plan p;
-  if ((st = plan_grad(grouped ? G : 0, M, N, K, s, p)) != BST_OK) return st;
-  if ((st = check_ws(p, ws, ws_bytes)) != BST_OK) return st;
   const int kind = dy == BST_BF16 ? DY_BF16 : dy == BST_F16 ? DY_F16 : DY_F32;
+  if ((st = plan_grad(grouped ? G : 0, M, N, K, kind + 1, s, p)) != BST_OK) return st;
+  if ((st = check_ws(p, ws, ws_bytes)) != BST_OK) return st;
   const BlockGradList l = block_grad_list();
   const BlockGradInstance* in = nullptr;
   for (int i = 0; i < l.count && !in; ++i)
@@ -608,9 +610,16 @@ size_t bst_block_workspace_bytes(int kind, int64_t count, int64_t M, int64_t N, 
     return 0;
   }
   if ((kind == 0 || kind == 3) && takes_rows(kind == 3, M, N, K, s)) return 0;
-  if (kind == 1 || kind == 2)
-    return plan_grad(kind == 2 ? count : 0, M, N, K, s, p) == BST_OK ? p.ws : 0;
-  // the output type, which may change the tile, is not known here: enough for any
+  // the types, which may change the tile or the split, are not known here:
+  // enough for any
+  if (kind == 1 || kind == 2) {
+    size_t most = 0;
+    for (int parts = 1; parts <= 3; ++parts) {
+      Plan q;
+      if (plan_grad(kind == 2 ? count : 0, M, N, K, parts, s, q) == BST_OK) most = std::max(most, q.ws);
+    }
+    return most;
+  }
   Plan q;
   const bst_status other = plan_gemm(0, M, N, K, true, s, q);
   const bst_status st = plan_gemm(0, M, N, K, false, s, p);

@@ -176,11 +176,11 @@ __global__ void __launch_bounds__(512) block_rows_kernel(BlockGemmArgs a) {
 // takes 32 columns; its eight waves share out the blocks of K, and each runs
 // a pipeline of its own (DMA of the wave's next 128 x 32 patches into its own
 // LDS buffers while it multiplies one), so that the loop has no barrier and the
-// time is a few memory latencies (33 rows, 4112 x 2056: with two buffers 7.8 us, with four 6.8).  The 32-byte rows of
-// a patch share their cache lines with the neighbours', which run on the same
-// die.  64 columns were slower (33 rows, 4112 x 2056: 8.4 us against 7.0), and
-// so were 16 waves (9.8).  A comes straight from memory: a lane's 32 bytes of
-// each half block.
+// time is a few memory latencies (33 rows, 4112 x 2056: 7.8 us with two buffers
+// a wave, 6.8 with four).  The 32-byte rows of a patch share their cache lines
+// with the neighbours', which run on the same die.  With two buffers, 64
+// columns a workgroup were slower (8.4 us against 7.0), and so were 16 waves
+// (9.8).  A comes straight from memory: a lane's 32 bytes of each half block.
 template <int FM, bool EXACT>
 struct BlockRowsN {
   static constexpr int NW = 8, BN = 32, DEPTH = 4;
