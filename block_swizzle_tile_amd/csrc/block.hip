@@ -230,14 +230,15 @@ bst_status plan_grad(int64_t count, int64_t M, int64_t N, int64_t K, int parts, 
 //   1 x 1024 x 8192 7.6 / 8.1, 1 x 2048 x 14336 11.6 / 10.0 (the one loss of
 //   the rule), 1 x 16384 x 4096 16.0 / 14.8;
 // K x N weights: 1 x 4096 x 4096 7.2 / 7.9, 1 x 4096 x 8192 14.1 / 9.8,
-//   32 x 8192 x 2048 6.9 / 9.9, 33 x 4112 x 2056 6.8 / 9.7,
+//   32 x 8192 x 2048 6.9 / 9.9, 33 x 4112 x 2056 6.4 / 9.7,
 //   33 x 4096 x 4096 11.7 / 10.5, 1 x 14336 x 2048 10.6 / 8.9.
 bool takes_rows(int32_t trans_b, int64_t M, int64_t N, int64_t K, const Sched& s) {
   if (s.tm != 0 || s.tn != 0 || s.split != 0) return false;
   const int64_t nk = cdiv(K, 128), cus = device_cu_count();
   if (trans_b)
     return M <= 32 && M * nk <= 768 && cdiv(N, 128) * 2 < cus;
-  return M <= 64 && nk <= (M <= 32 ? 32 : 24) && cdiv(N, 32) <= cus;
+  constexpr int64_t most = BlockRowsN<1, false>::MOST;
+  return M <= 64 && nk <= (M <= 32 ? most : most * 3 / 4) && cdiv(N, 32) <= cus;
 }
 
 bst_status check_ws(const Plan& p, const void* ws, size_t bytes) {

@@ -173,17 +173,19 @@ __global__ void __launch_bounds__(512) block_rows_kernel(BlockGemmArgs a) {
 // ------------------------------------------------------- weights K x N ----
 // The same for weights whose rows run along N: an operand then has to be
 // gathered from 128 rows, which the transposing LDS reads do.  A workgroup
-// takes 32 columns; its eight waves share out the blocks of K, and each runs
-// a pipeline of its own (DMA of the wave's next 128 x 32 patches into its own
-// LDS buffers while it multiplies one), so that the loop has no barrier and the
-// time is a few memory latencies (33 rows, 4112 x 2056: 7.8 us with two buffers
-// a wave, 6.8 with four).  The 32-byte rows of a patch share their cache lines
-// with the neighbours', which run on the same die.  With two buffers, 64
-// columns a workgroup were slower (8.4 us against 7.0), and so were 16 waves
-// (9.8).  A comes straight from memory: a lane's 32 bytes of each half block.
+// takes 32 columns; its eight waves share out the blocks of K, and each asks
+// for all of its 128 x 32 patches (up to four, by DMA into its own LDS buffers)
+// before it multiplies the first, so that the time is about one memory latency
+// (33 rows, 4112 x 2056: 7.8 us with two buffers a wave, 6.4 with four) and
+// there is no barrier before the sums.  The 32-byte rows of a patch share their
+// cache lines with the neighbours', which run on the same die.  With two
+// buffers, 64 columns a workgroup were slower (8.4 us against 7.0), and so were
+// 16 waves (9.8).  A comes straight from memory: a lane's 32 bytes of each half
+// block.
 template <int FM, bool EXACT>
 struct BlockRowsN {
   static constexpr int NW = 8, BN = 32, DEPTH = 4;
+  static constexpr int MOST = NW * DEPTH;  // blocks of K: a buffer for every patch
   static constexpr int BUF = 128 * BN;  // a patch
   static constexpr int SUMS = FM * 32 * BN * 4;  // a wave's partial sums
   static constexpr int LDS_BYTES = NW * (DEPTH * BUF > SUMS ? DEPTH * BUF : SUMS);
@@ -207,11 +209,10 @@ struct BlockRowsN {
   // come on top).
   static constexpr int QUEUED = DMAS + 4 * FM;
   static_assert((DEPTH - 1) * QUEUED < 64, "vmcnt holds 6 bits");
-  // The oldest patch has landed, with `later` (at most) others behind it, and
-  // what was read from its buffer before has arrived.
+  // The oldest patch has landed, with LATER others behind it.
   template <int LATER>
   static __device__ __forceinline__ void wait_for() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LATER * QUEUED) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER * QUEUED) : "memory");
   }
 
   __device__ __attribute__((always_inline)) static void run(const BlockGemmArgs& a) {
@@ -312,28 +313,23 @@ struct BlockRowsN {
       }
     };
 
-    // patch t of the wave is block wave + t NW of K, in buffer t % DEPTH
-    const uint32_t mine_n = wave < a.nk ? (a.nk - wave + NW - 1) / NW : 0u;
+    // patch t of the wave is block wave + t NW of K, in buffer t
+    const uint32_t count = wave < a.nk ? (a.nk - wave + NW - 1) / NW : 0u;
     Rest rest[DEPTH];
     static_for<DEPTH>([&](auto u) {
       constexpr uint32_t U = decltype(u)::value;
-      if (U < mine_n) fetch(wave + U * NW, U, rest[U]);
+      if (U < count) fetch(wave + U * NW, U, rest[U]);
     });
-    for (uint32_t t = 0; t < mine_n; t += DEPTH)
-      static_for<DEPTH>([&](auto u) {
-        constexpr uint32_t U = decltype(u)::value;
-        if (t + U >= mine_n) return;
-        const uint32_t later = mine_n - 1 - (t + U);
-        if (later >= 3) wait_for<3>();
-        else if (later == 2) wait_for<2>();
-        else if (later == 1) wait_for<1>();
-        else wait_for<0>();
-        multiply(wave + (t + U) * NW, U, rest[U]);
-        if (t + U + DEPTH < mine_n) {
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the buffer's reads have arrived
-          fetch(wave + (t + U + DEPTH) * NW, U, rest[U]);
-        }
-      });
+    static_for<DEPTH>([&](auto u) {
+      constexpr uint32_t U = decltype(u)::value;
+      if (U >= count) return;
+      const uint32_t later = count - 1 - U;
+      if (later >= 3) wait_for<3>();
+      else if (later == 2) wait_for<2>();
+      else if (later == 1) wait_for<1>();
+      else wait_for<0>();
+      multiply(wave + U * NW, U, rest[U]);
+    });
     // ---- the waves' sums, each in rows of BN columns whose 4-column chunks
     // are XORed by the row, then added in wave order
     constexpr uint32_t QPR = BN / 4;

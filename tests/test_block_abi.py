@@ -243,3 +243,6 @@ def test_refuses_more_than_a_launch_holds(L):
     wide = dict(M=128, N=1 << 17, K=1 << 17, ldq=1 << 17, lds=1 << 10, sched=S(split_k=2))
     assert grad(L, **wide) == _lib.E_INVAL
     assert b"too large" in L.bst_last_error()
+    # 64 rows of Q span 2 GiB
+    assert grad(L, ldq=1 << 25) == _lib.E_UNSUPPORTED
+    assert grad(L, ldq=(1 << 25) - 16, dY=None) == _lib.E_INVAL     # (accepted, and dY is not)

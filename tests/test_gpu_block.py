@@ -249,6 +249,45 @@ def test_offsets_past_32_bits():
     assert torch.equal(wide(q, s), wide(A, sa))
 
 
+
+def test_wide_pitches():
+    """Outputs and gradients whose pitch is past the 31-bit offsets of the vector paths: 256 rows of
+    C and 64 rows of dY span 2 GiB and more, though only a few rows are there."""
+    g = gen(3)
+    M, N, K = 5, 48, 272
+    A, sa, B, sb = operands(M, N, K, False, ("e8m0", "f32"), g)
+    ref, den = ref_product(A, sa, B, sb, False)
+    cut = cut_product(A, sa, B, sb, False)
+    for out, pitch in ((BF, 1 << 22), (FF, 1 << 21)):
+        C = torch.full((M, pitch), 7.0, dtype=out, device="cuda")
+        for tile in ((0, 0), (64, 128), (128, 128)):
+            bst.gemm_block_scaled(A, B, sa, sb, C[:, :N], sched=bst.make_sched(tile=tile, split_k=1))
+            check_sum(C[:, :N], ref, den, K, out, str(tile), cut)
+        assert bool((C[:, N:] == 7).all())
+    q, s = bst.quant_block(torch.randn(M, K, generator=g, device="cuda"))
+    for dtype, pitch in ((BF, 1 << 24), (FF, 1 << 23)):
+        dY = torch.randn(M, pitch, generator=g, device="cuda", dtype=dtype)[:, :N]
+        x = wide(q, s)
+        check_sum(bst.weight_grad(q, s, dY), x.t() @ dY.double(), x.abs().t() @ dY.double().abs(),
+                  3 * M, FF)
+
+
+@pytest.mark.parametrize("tb", [False, True])
+def test_few_rows_boundaries(tb):
+    """Row counts and lengths of K on both sides of where the kernels for a few rows begin and
+    end, with one patch of K per wave and with several, whole and cut short."""
+    for M in (1, 16, 17, 32, 33, 64, 65):
+        for K in (1, 127, 128, 1024, 1025, 2047, 2944, 2960, 4081, 4096, 4112):
+            g = gen(M * 8192 + K)
+            N = 72
+            A, sa, B, sb = operands(M, N, K, tb, ("f32", "e8m0"), g)
+            for out in (BF, FF):
+                say("few rows", tb, M, K, out)
+                C = bst.gemm_block_scaled(A, B, sa, sb, trans_b=tb, out_dtype=out)
+                ref, den = ref_product(A, sa, B, sb, tb)
+                check_sum(C, ref, den, K, out, "", cut_product(A, sa, B, sb, tb))
+
+
 # -------------------------------------------------------------- products ---
 TILES = [(32, 128), (64, 128), (128, 128), (256, 256)]
 KINDS = [("e8m0", "e8m0"), ("f32", "f32"), ("e8m0", "f32"), ("f32", "e8m0")]
