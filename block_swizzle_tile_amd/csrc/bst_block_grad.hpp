@@ -178,7 +178,8 @@ struct BlockGrad {
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
       const uint32_t id = i * NT + threadIdx.x, r = id / XCH, ch = id % XCH;
-      const float s = __builtin_bit_cast(float, h.e[i] << 23);  // the exponent field is what counts
+      // the conversion reads only the exponent field: 0 is 2^-127, and 255 gives NaN
+      const float s = __builtin_bit_cast(float, h.e[i] << 23);
       uint32_t o[8];
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
