@@ -8,12 +8,20 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 # BST_LIB selects another build of the same library (the sanitizer build of the
 # CPU tests); there is no other library and no fallback
 LIB_PATH = os.environ.get("BST_LIB") or os.path.join(PKG, "libbst.so")
+
+
+
+def fast_path(torch_version):
+    """File of the extension module built for this Python and that torch (build.py, block.py)."""
+    return os.path.join(PKG, "_block_fast-%s-torch%s.so" % (sys.implementation.cache_tag, torch_version))
+
 
 # bst_status
 OK, E_INVAL, E_UNSUPPORTED, E_ALIGN, E_WORKSPACE, E_HIP = 0, -1, -2, -3, -4, -5

@@ -28,7 +28,7 @@ import os
 
 import torch
 
-from ._lib import BF16, F16, F32, PKG, Sched, check, lib
+from ._lib import BF16, F16, F32, Sched, check, fast_path, lib
 
 E8M0 = 8
 
@@ -43,7 +43,7 @@ _CODES = torch.float8_e4m3fn
 
 _L = None
 _fast_module = None
-FAST_PATH = os.path.join(PKG, "_block_fast.so")
+FAST_PATH = fast_path(torch.__version__)
 
 
 def _fast():
@@ -55,7 +55,7 @@ def _fast():
 def _load_fast():
     global _fast_module
     if not os.path.exists(FAST_PATH):
-        raise RuntimeError("_block_fast.so is not built (%s); run "
+        raise RuntimeError("_block_fast is not built for this torch (%s); run "
                            "`python -m block_swizzle_tile_amd.build`" % FAST_PATH)
     loader = importlib.machinery.ExtensionFileLoader("_block_fast", FAST_PATH)
     m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_block_fast", loader))

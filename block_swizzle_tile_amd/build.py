@@ -19,9 +19,9 @@ DEPS = ([os.path.join(CSRC, f) for f in SOURCES + HEADERS] +
         [os.path.join(ROOT, "include", f) for f in ("bst.h", "bst_block.h")])
 LIB = os.path.join(PKG, "libbst.so")
 # The short way from Python to the block-scaled operators: host code only,
-# against torch's and Python's headers.
+# against torch's and Python's headers, so its file is named after both
+# (_lib.fast_path).  libbst.so needs neither.
 FAST_SOURCE = os.path.join(CSRC, "block_fast.cpp")
-FAST_LIB = os.path.join(PKG, "_block_fast.so")
 # The same kernels with cycle accounting (-DBST_TRACE): per-wave K-loop and
 # task phase cycles of workgroup 0 and a per-workgroup shader-clock record,
 # written to a device buffer set with bst_debug_set_trace.  For measurement
@@ -36,8 +36,9 @@ HIPCC_FLAGS = [
 
 
 def build(force: bool = True, verbose: bool = False, trace: bool = False) -> str:
-    """Compile libbst.so (always when force, else only when a source is newer);
-    trace=True builds libbst_trace.so instead."""
+    """Compile libbst.so (always when force, else only when a source is newer), which takes hipcc
+    alone, and _block_fast for the torch that is importable, if any: a failure of that is raised
+    after libbst.so is in place.  trace=True builds libbst_trace.so instead."""
     lib = TRACE_LIB if trace else LIB
     fast = _start_fast(force) if not trace else None
     if not force and os.path.exists(lib) and all(
@@ -78,16 +79,23 @@ def build(force: bool = True, verbose: bool = False, trace: bool = False) -> str
 
 
 def _start_fast(force):
-    """Starts compiling _block_fast.so; None if it is up to date."""
+    """Starts compiling _block_fast: (file, temporary file, process).  None if it is up to date or
+    there is no torch to bind; a text if it cannot be started."""
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError as e:
+        print("torch is not importable (%s): _block_fast is not built" % e, file=sys.stderr)
+        return None
+    from ._lib import fast_path
+    out = fast_path(torch.__version__)
     deps = [FAST_SOURCE] + [os.path.join(ROOT, "include", f) for f in ("bst.h", "bst_block.h")]
-    if not force and os.path.exists(FAST_LIB) and all(
-            os.path.getmtime(FAST_LIB) >= os.path.getmtime(d) for d in deps):
+    if not force and os.path.exists(out) and all(
+            os.path.getmtime(out) >= os.path.getmtime(d) for d in deps):
         return None
     import sysconfig
 
-    import torch
-    from torch.utils import cpp_extension
-    tmp = FAST_LIB + ".tmp%d" % os.getpid()
+    tmp = out + ".tmp%d" % os.getpid()
     inc = cpp_extension.include_paths() + ["/opt/rocm/include", sysconfig.get_paths()["include"],
                                            os.path.join(ROOT, "include")]
     cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
@@ -95,18 +103,24 @@ def _start_fast(force):
            [x for i in inc for x in ("-isystem" if "torch" in i else "-I", i)] +
            [FAST_SOURCE, "-o", tmp, "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
             "-ltorch_python", "-ltorch_cpu", "-ltorch_hip", "-lc10_hip", "-lc10"])
-    return tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    try:
+        pr = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    except OSError as e:
+        return str(e)
+    return out, tmp, pr
 
 
 def _finish_fast(started):
     if started is None:
         return
-    tmp, pr = started
+    if isinstance(started, str):
+        raise RuntimeError("_block_fast was not built: " + started)
+    lib, tmp, pr = started
     out, _ = pr.communicate()
     if pr.returncode != 0:
         sys.stderr.write(out)
-        raise RuntimeError("g++ failed building _block_fast.so")
-    os.replace(tmp, FAST_LIB)
+        raise RuntimeError("g++ failed building " + os.path.basename(lib))
+    os.replace(tmp, lib)
 
 
 if __name__ == "__main__":
