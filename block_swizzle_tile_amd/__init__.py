@@ -18,6 +18,7 @@ gradients) are in :mod:`.block` and reached from here by the same names.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 
 from ._lib import (BF16, E4M3, F16, F32, I8, I32, MXE4M3, BstError, Sched, check, lib,  # noqa: F401
                    LIB_PATH)
@@ -28,13 +29,14 @@ _DIRS = {"zn": ZN, "nz": NZ, "raster": RASTER}
 __all__ = ["Sched", "BstError", "make_sched", "gemm", "gemm_padded", "batched_gemm",
            "grouped_gemm_slice_m", "grouped_gemm_slice_k",
            "quant_gemm_per_token", "tile_map", "grouped_tile_map", "workspace_bytes",
-           "effective_sched", "task_count", "clock_record", "version", "LIB_PATH",
-           "quant_block", "dequant_block", "gemm_block_scaled", "grouped_gemm_block_scaled",
-           "weight_grad", "grouped_weight_grad", "block_workspace_bytes"]
+           "effective_sched", "task_count", "clock_record", "version", "LIB_PATH"]
 
-# the block-scaled operators' binding imports torch: on first use, like the rest of the package
-_BLOCK = {"quant_block", "dequant_block", "gemm_block_scaled", "grouped_gemm_block_scaled",
-          "weight_grad", "grouped_weight_grad", "block_workspace_bytes"}
+# the block-scaled operators' binding imports torch: on first use, like the rest of the package,
+# and `import *`, which uses every name, gives theirs where there is a torch
+_BLOCK = ["quant_block", "dequant_block", "gemm_block_scaled", "grouped_gemm_block_scaled",
+          "weight_grad", "grouped_weight_grad", "block_workspace_bytes"]
+if importlib.util.find_spec("torch") is not None:
+    __all__ += _BLOCK
 
 
 def __getattr__(name):
