@@ -87,8 +87,9 @@ bst_status launched(hipError_t e, const char* what) {
 }
 
 // A launch holds fewer than 2^32 threads.
+bool grid_fits(int64_t workgroups, int64_t threads) { return workgroups <= 0xffffffffLL / threads; }
 bst_status grid_ok(int64_t workgroups, int64_t threads) {
-  if (workgroups <= 0xffffffffLL / threads) return BST_OK;
+  if (grid_fits(workgroups, threads)) return BST_OK;
   return set_error(BST_E_UNSUPPORTED, "%lld workgroups of %lld threads are more than one launch holds",
                    (long long)workgroups, (long long)threads);
 }
@@ -200,9 +201,12 @@ bst_status plan_grad(int64_t count, int64_t M, int64_t N, int64_t K, int parts, 
   const int64_t stages = std::max<int64_t>(cdiv(cdiv(M, G), 64), 1);
   const double slice = (double)G * K * N * 8 / 5e6 + 0.07;
   double best = -1;
+  int64_t fewest = 0;
   for (int64_t tile = 128; tile <= 256; tile += 128) {
     if (s.tm != 0 && s.tm != tile) continue;
     const int64_t tiles = G * cdiv(K, tile) * cdiv(N, tile);
+    fewest = tiles;
+    if (!grid_fits(tiles, 512)) continue;  // 64 times the others stay in 64 bits
     const double stage = kStage[parts - 1][tile / 256];
     for (int64_t n = 1; n <= std::min<int64_t>(s.split ? s.split : 32, stages); ++n) {
       if (s.split && n != std::min<int64_t>(s.split, stages)) continue;
@@ -216,6 +220,7 @@ bst_status plan_grad(int64_t count, int64_t M, int64_t N, int64_t K, int parts, 
       }
     }
   }
+  if (best < 0) return grid_ok(fewest, 512);
   return plan_workspace(p, G * K, N);
 }
 

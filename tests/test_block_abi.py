@@ -246,3 +246,17 @@ def test_refuses_more_than_a_launch_holds(L):
     # 64 rows of Q span 2 GiB
     assert grad(L, ldq=1 << 25) == _lib.E_UNSUPPORTED
     assert grad(L, ldq=(1 << 25) - 16, dY=None) == _lib.E_INVAL     # (accepted, and dY is not)
+
+
+def test_gradient_tiles_past_64_bits(L):
+    """1024 groups of the largest weights in 64 slices, 2^64 workgroups and more, are counted and
+    refused (under the undefined-behaviour sanitizer too: test_block_sanitizers.py)."""
+    big = (1 << 31) - 1
+    for split in (0, 1, 2, 64):
+        s = bst.make_sched(split_k=split)
+        assert L.bst_block_workspace_bytes(2, 1024, 1 << 30, big, big, ctypes.byref(s)) == 0
+    K = 1 << 20
+    for split in (0, 1):
+        assert L.bst_grouped_weight_grad(BF, FF, 1024, P, 1 << 22, K, K, P, K, P, K // 128, P, K, None, 0, 0,
+                                         P, K, K * K, S(split_k=split), None, 0, None) == _lib.E_UNSUPPORTED
+        assert b"one launch" in L.bst_last_error()
