@@ -267,7 +267,6 @@ bst_status reduce(const Plan& p, int64_t count, int64_t rows, int64_t N, const f
   r.ldadd = ldadd;
   r.strideadd = strideadd;
   r.split = p.split;
-  r.count = (uint32_t)count;
   r.rows = (uint32_t)rows;
   r.cols = (uint32_t)N;
   r.pitch = p.pitch;

@@ -16,8 +16,6 @@ int device_cu_count();
 
 constexpr uint32_t kScaleBlock = 128;  // values that share a scale
 
-enum ScaleKind { SCALE_E8M0 = 8, SCALE_F32 = 7 };
-
 // 2^(e - 127); byte 0 is the subnormal 2^-127, byte 255 NaN.
 __device__ __forceinline__ float e8m0_value(uint32_t e) {
   const uint32_t bits = e == 0u ? 0x00400000u : e == 255u ? 0x7fc00000u : e << 23;
@@ -332,7 +330,7 @@ struct ReduceArgs {
   uint8_t* dst;
   const uint8_t* add;
   int64_t ld, stride, ldadd, strideadd;  // elements
-  uint32_t split, count, rows, cols, pitch;
+  uint32_t split, rows, cols, pitch;
   uint32_t kind, vec;
   FastDiv quads, by_rows;  // pitch / 4, rows
   uint32_t total;          // count * rows * pitch / 4

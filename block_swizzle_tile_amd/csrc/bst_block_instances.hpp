@@ -13,10 +13,7 @@ namespace bst {
 
 struct BlockGemmInstance {
   int bm, bn;
-  bool tb;
   int mode;  // BlockMode
-  bool grouped;
-  int threads;
   hipError_t (*launch)(uint32_t grid, hipStream_t, const BlockGemmArgs&);
 };
 struct BlockGemmList {
@@ -29,7 +26,7 @@ BlockGemmList block_gemm_grouped_t();
 BlockGemmList block_gemm_grouped_n();
 
 struct BlockGradInstance {
-  int bk, bn, dy, depth;
+  int bk, bn, dy;
   hipError_t (*launch)(uint32_t grid, hipStream_t, const BlockGradArgs&);
 };
 struct BlockGradList {
@@ -52,10 +49,9 @@ hipError_t launch_block_grad(uint32_t grid, hipStream_t st, const BlockGradArgs&
   return hipGetLastError();
 }
 
-#define BST_BLOCK_GEMM(BM, BN, WM, WN, ST, TB, MODE, GR)    \
-  BlockGemmInstance {                                       \
-    BM, BN, TB, MODE, GR, 64 * WM * WN,                     \
-        &launch_block_gemm<BM, BN, WM, WN, ST, TB, MODE, GR> \
+#define BST_BLOCK_GEMM(BM, BN, WM, WN, ST, TB, MODE, GR)                \
+  BlockGemmInstance {                                                   \
+    BM, BN, MODE, &launch_block_gemm<BM, BN, WM, WN, ST, TB, MODE, GR> \
   }
 #define BST_BLOCK_GEMM_TILE(BM, BN, WM, WN, ST, TB, GR)     \
   BST_BLOCK_GEMM(BM, BN, WM, WN, ST, TB, MODE_E8M0, GR),    \
@@ -67,6 +63,6 @@ hipError_t launch_block_grad(uint32_t grid, hipStream_t st, const BlockGradArgs&
       BST_BLOCK_GEMM(256, 256, 2, 4, 2, TB, MODE_E8M0, GR), BST_BLOCK_GEMM(256, 256, 2, 4, 2, TB, MODE_F32, GR)
 
 #define BST_BLOCK_GRAD(BK, BN, WM, WN, DY) \
-  BlockGradInstance { BK, BN, DY, BlockGrad<BK, BN, WM, WN, DY>::D, &launch_block_grad<BK, BN, WM, WN, DY> }
+  BlockGradInstance { BK, BN, DY, &launch_block_grad<BK, BN, WM, WN, DY> }
 
 }  // namespace bst
