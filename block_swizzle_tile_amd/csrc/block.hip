@@ -141,6 +141,10 @@ bst_status plan_workspace(Plan& p, int64_t rows, int64_t N) {
 }
 
 // Tile and split of a product.  count: groups (0: plain); exact: an fp32 output.
+// The large tile goes by all rows, also where a group's rows fill half of it:
+// its longer reuse of the weights outweighs the idle half (8192 rows over 64
+// groups, N 4096, K 2048, E8M0: 256x256 166 us, 128x128 200, 64x128 279; N 2048,
+// K 4096: 180, 183, 245; over 8 groups of N 4096, K 2048: 86, 126, 182).
 bst_status plan_gemm(int64_t count, int64_t M, int64_t N, int64_t K, bool exact, const Sched& s,
                      Plan& p) {
   const int64_t cus = device_cu_count(), G = std::max<int64_t>(count, 1);
@@ -171,8 +175,9 @@ bst_status plan_gemm(int64_t count, int64_t M, int64_t N, int64_t K, bool exact,
     split = 1;
   } else if (split == 0) {
     split = 1;
-    // one workgroup per CU: beyond that a split only adds partial sums (one row,
-    // 4096 x 4096: 10.3 us at half the CUs, 9.2 at all, 13.4 at twice)
+    // one workgroup per CU: beyond that a split only adds partial sums (one row
+    // on the 32x128 tile, 4096 x 4096: 10.3 us at half the CUs, 9.2 at all, 13.4
+    // at twice)
     if (p.tiles > 0 && p.tiles < cus && nk >= 4)
       split = std::max<int64_t>(1, std::min<int64_t>({cus / p.tiles, nk / 2, 16}));
   }
@@ -228,15 +233,20 @@ bst_status plan_grad(int64_t count, int64_t M, int64_t N, int64_t K, int parts, 
 // asked for.  They need one launch and no partial sums, but a workgroup walks
 // all of K and reads all of A, so they lose to a split where K is long or the
 // rows are many, and to unsplit tiles where the columns are many.  Times in us,
-// these kernels against the tiles, M x N x K:
+// these kernels against the tiles, M x N x K (sizes that the rule leaves to the
+// tiles among them):
 // N x K weights: 1 x 4096 x 4096 5.2 / 9.2, 1 x 4096 x 14336 12.8 / 14.6,
 //   16 x 4096 x 6144 8.9 / 9.9, 16 x 4096 x 8192 12.2 / 10.5,
 //   32 x 4096 x 2944 7.3 / 9.9, 32 x 4096 x 4096 10.6 / 10.0,
-//   1 x 1024 x 8192 7.6 / 8.1, 1 x 2048 x 14336 11.6 / 10.0 (the one loss of
-//   the rule), 1 x 16384 x 4096 16.0 / 14.8;
+//   1 x 1024 x 8192 7.6 / 8.1, 1 x 2048 x 14336 10.7 / 11.3, 1 x 256 x 4096
+//   4.6 / 7.5, 1 x 16384 x 4096 16.0 / 14.8; the rule loses where a row's K is
+//   longer still and the columns are few: 1 x 512 x 16384 11.5 / 10.3,
+//   1 x 1024 x 28672 18.6 / 13.9, 1 x 512 x 32768 20.6 / 14.2;
 // K x N weights: 1 x 4096 x 4096 7.2 / 7.9, 1 x 4096 x 8192 14.1 / 9.8,
 //   32 x 8192 x 2048 6.9 / 9.9, 33 x 4112 x 2056 6.4 / 9.7,
-//   33 x 4096 x 4096 11.7 / 10.5, 1 x 14336 x 2048 10.6 / 8.9.
+//   33 x 4096 x 4096 11.7 / 10.5, 1 x 14336 x 2048 10.6 / 8.9; few columns:
+//   1 x 256 x 4096 5.7 / 7.3, 32 x 256 x 4096 9.1 / 8.2 (a loss of the rule),
+//   64 x 512 x 2944 9.8 / 9.6.
 bool takes_rows(int32_t trans_b, int64_t M, int64_t N, int64_t K, const Sched& s) {
   if (s.tm != 0 || s.tn != 0 || s.split != 0) return false;
   const int64_t nk = cdiv(K, 128), cus = device_cu_count();

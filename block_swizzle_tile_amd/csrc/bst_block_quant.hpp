@@ -18,7 +18,7 @@ struct BlockQuantArgs {
   uint8_t* S;        // scales (read or written)
   int64_t ldx, ldq, lds;
   uint32_t M, K, kb;   // kb: blocks per row
-  uint32_t blocks;     // M * kb, or block_rows = 128: ceil(M/128) * kb
+  uint32_t blocks;     // M * kb: runs of 128 in the rows, whatever shares a scale
   uint32_t xvec, qvec;  // rows of X / Q start on whole vectors
   uint32_t s_f32, block_rows;
   FastDiv by_kb;

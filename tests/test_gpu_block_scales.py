@@ -201,3 +201,17 @@ def test_grouped_weight_grad_many_slices(sizes, dtype):
                 a, b = x[lo:hi], dY[lo:hi].double()
                 check_sum(dW[k], a.t() @ b + add[k].double(), a.abs().t() @ b.abs() + add[k].double().abs(),
                           PARTS[dtype] * (hi - lo) + 1, FF, "group %d" % k)
+
+
+def test_restore_with_32_bit_scales():
+    """A code times a 32-bit scale is rounded to fp32, then to the type."""
+    g = gen(6)
+    q = torch.arange(256, device="cuda", dtype=torch.uint8).repeat(64, 2).view(torch.float8_e4m3fn)
+    for block_rows in (1, 128):
+        s = torch.exp(3 * torch.randn(64 if block_rows == 1 else 1, 4, generator=g, device="cuda"))
+        f = s.repeat_interleave(128, 1).expand(64, 512)
+        for out in (BF, HF, FF):
+            m = torch.finfo(out).max
+            v = q.float() * f
+            want = torch.where(v.isnan(), v, v.clamp(-m, m)).to(out)
+            assert same_values(bst.dequant_block(q, s, out_dtype=out, block_rows=block_rows), want), out
