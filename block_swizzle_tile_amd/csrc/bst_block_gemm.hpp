@@ -96,7 +96,7 @@ struct BlockGemm {
     __shared__ __attribute__((aligned(16))) uint8_t buf[LDS_BYTES];
     return (lds_t*)buf;
   }
-  static __device__ __forceinline__ uint32_t swz_b(uint32_t k) {
+  static __host__ __device__ __forceinline__ uint32_t swz_b(uint32_t k) {
     return ((k & 7u) + (k & 1u) * 8u) & BSWZ;
   }
 
@@ -120,9 +120,75 @@ struct BlockGemm {
   };
   static constexpr int RPB = TB ? 8 : 1024 / BN;
   // instruction x of wave w: its XOR and its first row (or K row)
-  static __device__ __forceinline__ uint32_t a_xor(uint32_t w, int x) { return (w * A_IPW + x) & 7u; }
-  static __device__ __forceinline__ uint32_t b_xor(uint32_t w, int x) {
+  static __host__ __device__ __forceinline__ uint32_t a_xor(uint32_t w, int x) {
+    return (w * A_IPW + x) & 7u;
+  }
+  static __host__ __device__ __forceinline__ uint32_t b_xor(uint32_t w, int x) {
     return TB ? (w * B_IPW + x) & 7u : ((w * B_IPW + x) * RPB) & 7u & BSWZ;
+  }
+
+  // What the addressing needs of a tile.  (It runs on the host too, where a test
+  // checks every access.)
+  struct Tile {
+    uint32_t lda32, ldb32, K;
+    uint32_t rows_left, cols_left;  // valid rows and columns
+    uint32_t s_pitch;  // bytes between the wave's scales: of two rows of A, or two blocks of columns
+    uint32_t blocks;   // blocks of columns from the tile's first on
+  };
+  static __host__ __device__ __forceinline__ Lanes lanes(const Tile& t, uint32_t wave, uint32_t lane) {
+    Lanes ln;
+    const uint32_t last = t.K & 127u;      // K rows of a partial last stage
+    constexpr int LPR = TB ? 8 : BN / 16;  // lanes per row of B
+    ln.a_row = (lane >> 3) * t.lda32;
+    ln.a_ch = (lane & 7u) ^ (lane >> 3);
+    ln.b_row = (lane / LPR) * t.ldb32;
+    ln.b_ch = (lane % LPR) ^ (TB ? lane >> 3 : swz_b(lane / LPR));
+    ln.inside = ln.tail = 0;
+#pragma unroll
+    for (int x = 0; x < A_IPW; ++x) {
+      const uint32_t r = (wave * A_IPW + x) * 8 + (lane >> 3), ch = ln.a_ch ^ a_xor(wave, x);
+      if (r < t.rows_left) ln.inside |= 1u << x;
+      if (r < t.rows_left && ch * 16 < last) ln.tail |= 1u << x;
+    }
+#pragma unroll
+    for (int x = 0; x < B_IPW; ++x) {
+      const uint32_t r = (wave * B_IPW + x) * RPB + lane / LPR, ch = ln.b_ch ^ b_xor(wave, x);
+      const uint32_t k = TB ? ch * 16 : r;
+      const bool in = TB ? r < t.cols_left : ch * 16 < t.cols_left;
+      if (in) ln.inside |= 1u << (A_IPW + x);
+      if (in && k < last) ln.tail |= 1u << (A_IPW + x);
+    }
+    if (wave < (uint32_t)SA_N)
+      ln.s_off = wave * 64 + lane < t.rows_left ? (wave * 64 + lane) * t.s_pitch : kOob;
+    else
+      ln.s_off = wave == (uint32_t)SA_N && lane < (BN + 127) / 128 && lane < t.blocks
+                     ? lane * t.s_pitch : kOob;
+    return ln;
+  }
+  // Bit x: access x of a lane is inside its matrix in stage kt of a slice that ends at kt1.
+  static __host__ __device__ __forceinline__ uint32_t live(const Lanes& ln, uint32_t kt, uint32_t kt1,
+                                                           uint32_t K) {
+    return kt >= kt1 ? 0u : (kt + 1) * 128u <= K ? ln.inside : ln.tail;
+  }
+  // Access X of a wave's lane: 16 bytes at lane + wave offset of A's panel (X <
+  // A_IPW) or B's, and where the wave's 1024 bytes go in the stage's LDS.
+  struct Access {
+    uint32_t voff, soff, lds;
+  };
+  template <int X>
+  static __host__ __device__ __forceinline__ Access access(uint32_t wave, uint32_t lda32, uint32_t ldb32,
+                                                           const Lanes& ln, uint32_t live_bits,
+                                                           uint32_t a_ch, uint32_t b_ch) {
+    if constexpr (X < A_IPW) {
+      const uint32_t off = ln.a_row + ((a_ch ^ a_xor(wave, X)) << 4);
+      return Access{(live_bits >> X) & 1u ? off : kOob, (wave * A_IPW + X) * 8 * lda32,
+                    (wave * A_IPW + X) * 1024};
+    } else {
+      constexpr int x = X - A_IPW;
+      const uint32_t off = ln.b_row + ((b_ch ^ b_xor(wave, x)) << 4);
+      return Access{(live_bits >> X) & 1u ? off : kOob, (wave * B_IPW + x) * RPB * ldb32,
+                    (uint32_t)A_BYTES + (wave * B_IPW + x) * 1024};
+    }
   }
 
   struct Src {
@@ -153,22 +219,14 @@ struct BlockGemm {
     st.base = lds() + s * STAGE_BYTES;
     st.a_ch = fresh_v(ln.a_ch);  // offsets are made anew for every stage, not kept
     st.b_ch = fresh_v(ln.b_ch);
-    st.live = kt >= c.kt1 ? 0u : (kt + 1) * 128u <= c.K ? ln.inside : ln.tail;
+    st.live = live(ln, kt, c.kt1, c.K);
     return st;
   }
   static constexpr int ND = A_IPW + B_IPW;
   template <int X>
   __device__ static __forceinline__ void dma_one(const Src& c, const Lanes& ln, const Stage& st) {
-    if constexpr (X < A_IPW) {
-      const uint32_t off = ln.a_row + ((st.a_ch ^ a_xor(c.wave, X)) << 4);
-      dma16(st.ra, st.base + (c.wave * A_IPW + X) * 1024, (st.live >> X) & 1u ? off : kOob,
-            (c.wave * A_IPW + X) * 8 * c.lda32);
-    } else {
-      constexpr int x = X - A_IPW;
-      const uint32_t off = ln.b_row + ((st.b_ch ^ b_xor(c.wave, x)) << 4);
-      dma16(st.rb, st.base + A_BYTES + (c.wave * B_IPW + x) * 1024,
-            (st.live >> X) & 1u ? off : kOob, (c.wave * B_IPW + x) * RPB * c.ldb32);
-    }
+    const Access m = access<X>(c.wave, c.lda32, c.ldb32, ln, st.live, st.a_ch, st.b_ch);
+    dma16(X < A_IPW ? st.ra : st.rb, st.base + m.lds, m.voff, m.soff);
   }
   __device__ static __forceinline__ void dma_scales(const Src& c, const Lanes& ln, const Stage& st,
                                                     uint32_t kt) {
@@ -583,33 +641,9 @@ struct BlockGemm {
     }
     c.lda32 = (uint32_t)a.lda;
     c.ldb32 = (uint32_t)a.ldb;
-    Lanes ln;
-    const uint32_t last = a.K & 127u;  // K rows of a partial last stage
-    constexpr int LPR = TB ? 8 : BN / 16;  // lanes per row of B
-    ln.a_row = (lane >> 3) * c.lda32;
-    ln.a_ch = (lane & 7u) ^ (lane >> 3);
-    ln.b_row = (lane / LPR) * c.ldb32;
-    ln.b_ch = (lane % LPR) ^ (TB ? lane >> 3 : swz_b(lane / LPR));
-    ln.inside = ln.tail = 0;
-#pragma unroll
-    for (int x = 0; x < A_IPW; ++x) {
-      const uint32_t r = (wave * A_IPW + x) * 8 + (lane >> 3), ch = ln.a_ch ^ a_xor(wave, x);
-      if (r < rows_left) ln.inside |= 1u << x;
-      if (r < rows_left && ch * 16 < last) ln.tail |= 1u << x;
-    }
-#pragma unroll
-    for (int x = 0; x < B_IPW; ++x) {
-      const uint32_t r = (wave * B_IPW + x) * RPB + lane / LPR, ch = ln.b_ch ^ b_xor(wave, x);
-      const uint32_t k = TB ? ch * 16 : r;
-      const bool in = TB ? r < cols_left : ch * 16 < cols_left;
-      if (in) ln.inside |= 1u << (A_IPW + x);
-      if (in && k < last) ln.tail |= 1u << (A_IPW + x);
-    }
-    if (for_a)
-      ln.s_off = wave * 64 + lane < rows_left ? (wave * 64 + lane) * (uint32_t)(a.ldsa * ss) : kOob;
-    else
-      ln.s_off = wave == (uint32_t)SA_N && lane < (BN + 127) / 128 && lane < nbs
-                     ? lane * (uint32_t)((TB ? a.ldsb : 1) * ss) : kOob;
+    const Tile tile{c.lda32, c.ldb32, a.K, rows_left, cols_left,
+                    (uint32_t)((for_a ? a.ldsa : TB ? a.ldsb : 1) * ss), nbs};
+    const Lanes ln = lanes(tile, wave, lane);
 
     f32x16_t acc[FM][FN];
 #pragma unroll

@@ -107,12 +107,13 @@ struct BlockGrad {
 
   // Offsets of a thread's loads from the stage's first row; past the tile's
   // columns they are out of every buffer's range, and such loads give zeros.
+  // (This runs on the host too, where a test checks every load.)
   struct Lanes {
     uint32_t x, e, y[DY == DY_F32 ? 2 : 1];
   };
-  __device__ static __forceinline__ Lanes lanes(const Src& c) {
-    const uint32_t xr = threadIdx.x / XCH, xc = threadIdx.x % XCH;
-    const uint32_t yr = threadIdx.x / YCH, yc = threadIdx.x % YCH * 8;
+  __host__ __device__ static __forceinline__ Lanes lanes(const Src& c, uint32_t tid) {
+    const uint32_t xr = tid / XCH, xc = tid % XCH;
+    const uint32_t yr = tid / YCH, yc = tid % YCH * 8;
     constexpr uint32_t ES = DY == DY_F32 ? 4 : 2, PER = 16 / ES;
     Lanes l;
     l.x = xc * 16 < c.kcols ? xr * (uint32_t)c.ldq + xc * 16 : kOob;
@@ -270,7 +271,7 @@ struct BlockGrad {
   template <bool VEC>
   __device__ static __forceinline__ void loop(f32x16_t (&acc)[FM][FN], const Src& c, uint32_t wm,
                                               uint32_t wn) {
-    const Lanes l = lanes(c);
+    const Lanes l = lanes(c, threadIdx.x);
     Held h;
     load<VEC>(h, c, l, 0);
     store(h, lds());

@@ -198,7 +198,33 @@ struct BlockRowsN {
   }
   // XOR of a row's chunks: rows 0..7 of a transposing read fall on all banks
   static constexpr int CPR = BN / 16, RPI = 64 / CPR, DMAS = 128 / RPI;
-  static __device__ __forceinline__ uint32_t swz_n(uint32_t k) { return (k >> 2) & 1u; }
+  static __host__ __device__ __forceinline__ uint32_t swz_n(uint32_t k) { return (k >> 2) & 1u; }
+
+  // A lane's part of the addressing (it runs on the host too, where a test checks
+  // every access).  DMA instruction x: K rows RPI x + lane / CPR, chunk lane % CPR
+  // of the patch.
+  struct Lane {
+    uint32_t k, off;  // first K row, and its offset from the patch's (kOob: past the columns)
+  };
+  static __host__ __device__ __forceinline__ Lane dma_lane(uint32_t lane, uint32_t ldb32, uint32_t cols) {
+    const uint32_t k = lane / CPR, ch = (lane % CPR) ^ swz_n(k);
+    return Lane{k, ch * 16 < cols ? k * ldb32 + ch * 16 : kOob};
+  }
+  // left: K rows from the patch's first on
+  static __host__ __device__ __forceinline__ uint32_t dma_voff(const Lane& l, int x, uint32_t left) {
+    return RPI * x + l.k < left ? l.off : kOob;
+  }
+  static __host__ __device__ __forceinline__ uint32_t dma_soff(int x, uint32_t ldb32) {
+    return (uint32_t)(RPI * x) * ldb32;
+  }
+  // transposing reads: K = 64 kk + 32 (t >> 1) + 16 hi + 8 (t & 1) + (L >> 1)
+  static __host__ __device__ __forceinline__ uint32_t read_off(uint32_t lane) {
+    const uint32_t L = lane & 15u, rk = 16 * (lane >> 5) + (L >> 1);
+    return rk * BN + ((((lane >> 4) & 1u) ^ swz_n(rk)) << 4) + 8 * (L & 1u);
+  }
+  static __host__ __device__ constexpr uint32_t read_step(int kk, int t) {
+    return (64 * kk + 32 * (t >> 1) + 8 * (t & 1)) * BN;
+  }
 
   // A's part of a patch.
   struct Rest {
@@ -222,12 +248,8 @@ struct BlockRowsN {
     const uint32_t cols = a.N - n0 < (uint32_t)BN ? a.N - n0 : BN;
     const int64_t sb = n0 / kScaleBlock;  // one block of columns: 32 divides 128
     lds_t* const own = lds() + wave * (DEPTH * BUF);
-    // DMA instruction x: K rows RPI x + lane / CPR, chunk lane % CPR of the patch
-    const uint32_t dk = lane / CPR, dch = (lane % CPR) ^ swz_n(dk);
-    const uint32_t doff = dch * 16 < cols ? dk * (uint32_t)a.ldb + dch * 16 : kOob;
-    // transposing reads: K = 64 kk + 32 (t >> 1) + 16 hi + 8 (t & 1) + (L >> 1)
-    const uint32_t L = lane & 15u, rk = 16 * hi + (L >> 1);
-    const uint32_t roff = rk * BN + ((((lane >> 4) & 1u) ^ swz_n(rk)) << 4) + 8 * (L & 1u);
+    const Lane dl = dma_lane(lane, (uint32_t)a.ldb, cols);
+    const uint32_t roff = read_off(lane);
     const bool sa_f32 = a.sa_f32 != 0, sb_f32 = a.sb_f32 != 0;
     const __amdgpu_buffer_rsrc_t ra = Rows::buffer(a.A), rsa = Rows::buffer(a.sa);
     uint32_t ao[FM], so[FM];
@@ -245,8 +267,7 @@ struct BlockRowsN {
       const u32x4_t d = make_desc(a.B + (int64_t)kb * 128 * a.ldb + n0);
 #pragma unroll
       for (int x = 0; x < DMAS; ++x)
-        dma16(d, own + s * BUF + x * 1024, RPI * x + dk < left ? doff : kOob,
-              (uint32_t)(RPI * x) * (uint32_t)a.ldb);
+        dma16(d, own + s * BUF + x * 1024, dma_voff(dl, x, left), dma_soff(x, (uint32_t)a.ldb));
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -289,7 +310,7 @@ struct BlockRowsN {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
           v[t] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-              (lds_i32x2_t*)(own + s * BUF + roff + (64 * kk + 32 * (t >> 1) + 8 * (t & 1)) * BN));
+              (lds_i32x2_t*)(own + s * BUF + roff + read_step(kk, t)));
         b[kk] = i32x8_t{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
       }
       const float fb = Rows::scale_value(n.sb, sb_f32);
