@@ -161,7 +161,8 @@ bst_status bst_weight_grad(bst_dtype dy, bst_dtype dw, int64_t M, int64_t N, int
 /*
  * bst_grouped_weight_grad -- one gradient per group of rows: dW_g = add_g +
  * X_g^T . dY_g over rows [P_g, P_g + group_m[g]) (as in
- * bst_grouped_gemm_block_scaled; groups of any size).  dW_g = dW +
+ * bst_grouped_gemm_block_scaled; groups of any size; where a few groups hold
+ * most rows, a schedule with xcd_remap = 0 is faster).  dW_g = dW +
  * g*stridedw, add_g = add + g*strideadd (elements).  An empty group's
  * gradient is add_g (or 0).  ws: bst_block_workspace_bytes(2, ...) bytes.
  */
