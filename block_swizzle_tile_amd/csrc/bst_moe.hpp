@@ -428,8 +428,10 @@ struct MoeGradArgs {
 // of dY against the same of each row.  Bound by memory: 8192 x 4 rows of 4096 bf16, 604
 // MB, 126 us, 4.8 TB/s; a small one by its chain of loads and the sum over the waves
 // (16 x 4 rows of 4096 bf16 5.1 us).
+template <int WPT>
+constexpr int kGradThreads = WPT == 1 ? 256 : 64 * WPT;
 template <int KIND, int WPT, bool FAR>
-__global__ void __launch_bounds__(WPT == 1 ? 256 : 64 * WPT) moe_combine_grad_kernel(MoeGradArgs a) {
+__global__ void __launch_bounds__(kGradThreads<WPT>) moe_combine_grad_kernel(MoeGradArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int ES = KIND == X_F32 ? 4 : 2, U = 4, N = kCols<KIND>;
   constexpr uint32_t kInd = KIND;

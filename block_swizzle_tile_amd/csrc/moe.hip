@@ -248,7 +248,9 @@ bst_status bst_moe_combine_grad(bst_dtype r, int64_t T, int32_t k, int64_t H, co
   // 9.4, 6.1).  Of few tokens every four choices are a task of their own (700 x 8 rows
   // of 2048 bf16: 10.7 us without, 9.6 with it, 1000 x 8 rows of 600 10.4, 7.7, of 2048
   // 13.5, 14.9), of sixteen waves where those leave CUs without work (20 x 6 rows of
-  // 7168 fp16: 11.9 us with a workgroup of four waves a token, 5.8).
+  // 7168 fp16: 11.9 us with a workgroup of four waves a token, 5.8; past the caches 256 x 4
+  // rows of 8192 bf16 18.7 us with four, 11.1 with sixteen, 64 x 8 rows of 8192 fp32 34.2,
+  // 15.8).
   const int64_t cus = device_cu_count(), lanes = cdiv(H * er, 16);  // that a row keeps busy
   const int64_t parts = T < cus * 4 && lanes > 64 ? cdiv(k, 4) : 1;
   const int waves = lanes > 256 && T * parts <= cus ? 16 : lanes >= 256 || (lanes > 64 && T < cus * 2) ? 4 : 1;
@@ -271,17 +273,19 @@ bst_status bst_moe_combine_grad(bst_dtype r, int64_t T, int32_t k, int64_t H, co
   a.wkind = (uint32_t)w;
   a.parts = (uint32_t)parts;
   a.by_parts = make_fastdiv(a.parts);
-  const dim3 grid((uint32_t)groups), block(64 * std::max(waves, 4));
-  auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, (hipStream_t)stream, a);
+  const bool far = is_far(T * k, H * er);
+  // a launch's threads are those of its kernel
+  auto run = [&](auto kind, auto wpt) {
+    constexpr int KIND = decltype(kind)::value, WPT = decltype(wpt)::value;
+    const dim3 grid((uint32_t)groups), block(kGradThreads<WPT>);
+    if (far) hipLaunchKernelGGL((moe_combine_grad_kernel<KIND, WPT, true>), grid, block, 0, (hipStream_t)stream, a);
+    else hipLaunchKernelGGL((moe_combine_grad_kernel<KIND, WPT, false>), grid, block, 0, (hipStream_t)stream, a);
     return launched(hipGetLastError(), "combine gradient");
   };
   auto pick = [&](auto kind) {
-    constexpr int KIND = decltype(kind)::value;
-    if (is_far(T * k, H * er))
-      return waves == 1 ? run(moe_combine_grad_kernel<KIND, 1, true>) : run(moe_combine_grad_kernel<KIND, 4, true>);
-    if (waves == 16) return run(moe_combine_grad_kernel<KIND, 16, false>);
-    return waves == 1 ? run(moe_combine_grad_kernel<KIND, 1, false>) : run(moe_combine_grad_kernel<KIND, 4, false>);
+    if (waves == 16) return run(kind, std::integral_constant<int, 16>{});
+    if (waves == 4) return run(kind, std::integral_constant<int, 4>{});
+    return run(kind, std::integral_constant<int, 1>{});
   };
   if (r == BST_F32) return pick(std::integral_constant<int, X_F32>{});
   if (r == BST_BF16) return pick(std::integral_constant<int, X_BF16>{});
