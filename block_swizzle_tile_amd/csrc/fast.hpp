@@ -8,6 +8,8 @@
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
+#include <ATen/record_function.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/hip/HIPFunctions.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -76,10 +78,17 @@ T* ptr(const at::Tensor& t) {
   return static_cast<T*>(t.data_ptr());
 }
 
-// An empty tensor on the inputs' device, without the dispatcher's way to it, unless
-// torch fills new tensors.
+// Whether anything listens to torch's dispatcher: a mode, a transform or a tracer (keys
+// of this thread beside those that are always there), or a profiler.
+inline bool heard() {
+  return !(c10::impl::tls_local_dispatch_key_set().included_ - c10::default_included_set).empty() ||
+         at::hasCallbacks();
+}
+
+// An empty tensor on the inputs' device, without the dispatcher's way to it (half a
+// microsecond), unless torch fills new tensors or something is there to see them.
 inline at::Tensor make(const at::Tensor& like, at::IntArrayRef shape, at::ScalarType type) {
-  if (at::globalContext().deterministicAlgorithms())
+  if (at::globalContext().deterministicAlgorithms() || heard())
     return at::empty(shape, like.options().dtype(type).requires_grad(false));
   return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
