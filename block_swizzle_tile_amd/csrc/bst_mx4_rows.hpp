@@ -10,7 +10,12 @@
 // and one.
 //
 // Grouped (a mixture of experts that serves a few tokens), a workgroup takes 16
-// columns of one group's weights, and the group's rows 16 FM at a time.
+// columns of one group's weights and 16 FM of its rows.  Every group has workgroups
+// for its first rows, found without looking at the others' sizes beyond the sum before
+// it; groups of more rows share those behind, so that one that gets all rows is spread
+// over the chip too (6144 rows over 256 groups of 16 x 7168: 10.5 us with 24 rows each, 18.2
+// with up to 406, 11.4 with all in one, and 10.5, 97 and 1419 where a workgroup went
+// through all rows of its group).
 #pragma once
 
 #include "bst_mx4_gemm.hpp"
@@ -57,13 +62,17 @@ struct Mx4Rows {
       const uint32_t tiles = (a.N + 15u) / 16u;
       g = tile / tiles;
       tile -= g * tiles;
-      // the group's rows: sizes below 0 count as 0, and groups are cut to M rows
-      int64_t before = 0;
-      for (uint32_t i = lane; i < g; i += 64u) before += max(a.group_m[i], 0);
-      for (int d = 32; d > 0; d >>= 1) before += __shfl_xor((long long)before, d);
-      if (before >= (int64_t)a.M) return;
-      row0 = __builtin_amdgcn_readfirstlane((uint32_t)before);
-      rows = min((uint32_t)max(a.group_m[g], 0), a.M - row0);
+      if (g < a.G) {
+        // the group's first rows: sizes below 0 count as 0, and groups are cut to M rows
+        int64_t before = 0;
+        for (uint32_t i = lane; i < g; i += 64u) before += max(a.group_m[i], 0);
+        for (int d = 32; d > 0; d >>= 1) before += __shfl_xor((long long)before, d);
+        if (before >= (int64_t)a.M) return;
+        row0 = __builtin_amdgcn_readfirstlane((uint32_t)before);
+        rows = min((uint32_t)max(a.group_m[g], 0), a.M - row0);
+      } else if (!later_rows(a, lane, g - a.G, g, row0, rows)) {
+        return;
+      }
       if (rows == 0) return;
     }
     const uint32_t n0 = tile * 16u, cols = min(a.N - n0, 16u);
@@ -71,13 +80,55 @@ struct Mx4Rows {
     const uint32_t bo = r * ldb + 32 * q, so = r * ldsb + 2 * q;
     const __amdgpu_buffer_rsrc_t rb = buffer(a.B + (int64_t)g * a.strideB + (int64_t)n0 * a.ldb, cols * ldb),
                                  rsb = buffer(a.sb + (int64_t)g * a.strideSB + (int64_t)n0 * a.ldsb, cols * ldsb);
-    for (uint32_t m0 = 0; m0 < rows; m0 += 16u * FM) {
-      if (GROUPED && m0 != 0) __syncthreads();  // (sums are read)
-      const int64_t arow = (int64_t)row0 + m0;
-      const uint32_t here = min(rows - m0, 16u * FM);
-      some_rows(a, sums, wave, lane, rb, rsb, buffer(a.A + arow * a.lda, here * lda),
-                buffer(a.sa + arow * a.ldsa, here * ldsa), bo, so, lda, ldsa, arow, here, n0);
+    const int64_t arow = row0;
+    const uint32_t here = min(rows, 16u * FM);
+    some_rows(a, sums, wave, lane, rb, rsb, buffer(a.A + arow * a.lda, here * lda),
+              buffer(a.sa + arow * a.ldsa, here * ldsa), bo, so, lda, ldsa, arow, here, n0);
+  }
+
+  // The sum of x over the lanes up to this one.
+  static __device__ __forceinline__ uint32_t sum_to_lane(uint32_t x) {
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xf, 0xf, false);  // 1, 2, 4 and 8 lanes
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xf, 0xf, false);  // back, in rows of 16
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xf, 0xf, false);
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xf, 0xf, false);
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xa, 0xf, false);  // a row's last to the next,
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xc, 0xf, false);  // the half's to the other
+    return x;
+  }
+
+  // Part `want` of the groups' rows behind their first 16 FM, in the order of the
+  // groups: its group, first row and the rows left from there.  False: there are not
+  // so many.  Each lane has a group, 64 at a time; sizes above M count as M, so that
+  // sums stay in 32 bits (M is at most 24 rows a group here).
+  static __device__ __forceinline__ bool later_rows(const Mx4GemmArgs& a, uint32_t lane, uint32_t want, uint32_t& g,
+                                                    uint32_t& row0, uint32_t& rows) {
+    // (mostly there are none, and the launch waits for all its workgroups)
+    uint64_t any = 0;
+    for (uint32_t g0 = 0; g0 < a.G; g0 += 64u) any |= __ballot(g0 + lane < a.G && a.group_m[g0 + lane] > 16 * FM);
+    if (any == 0) return false;
+    uint32_t before = 0;  // rows of the groups before these 64
+    for (uint32_t g0 = 0; g0 < a.G; g0 += 64u) {
+      const uint32_t n = g0 + lane < a.G ? min((uint32_t)max(a.group_m[g0 + lane], 0), a.M) : 0u;
+      const uint32_t end = before + sum_to_lane(n);
+      const uint32_t lo = min(end - n, a.M), mine = min(end, a.M) - lo;
+      const uint32_t parts = mine != 0 ? (mine - 1u) / (16u * FM) : 0u, last = sum_to_lane(parts);
+      const uint64_t past = __ballot(last > want);
+      if (past != 0) {
+        const int at = __builtin_ctzll(past);
+        const uint32_t skip = (1u + want - of_lane(last - parts, at)) * (16u * FM);
+        g = g0 + (uint32_t)at;
+        row0 = of_lane(lo, at) + skip;
+        rows = of_lane(mine, at) - skip;
+        return true;
+      }
+      before = of_lane(end, 63);
+      want -= of_lane(last, 63);
     }
+    return false;
+  }
+  static __device__ __forceinline__ uint32_t of_lane(uint32_t x, int lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
   }
 
   // Rows arow .. arow + here - 1 of A times the workgroup's columns.
@@ -139,7 +190,7 @@ struct Mx4Rows {
     for (int i = 0; i < FM; ++i) sums[i][wave][lane] = acc[i];
     __syncthreads();
     // wave w ends fragment w; lane l: row l & 15 of it, columns 4 (l >> 4) + 0..3
-    if (wave >= (uint32_t)FM) return;  // (from this function: the barriers are around it)
+    if (wave >= (uint32_t)FM) return;
     f32x4_t s = sums[wave][0][lane];
 #pragma unroll
     for (int w = 1; w < NW; ++w) s += sums[wave][w][lane];

@@ -106,13 +106,16 @@ bst_status plan_mx4(int64_t count, int64_t M, int64_t N, int64_t K, const Sched&
 //   4096 x 4096 7.0 / 8.0, 32 x 8192 x 2048 7.6 / 6.2 (left), 64 x 1024 x 1024
 //   4.2 / 5.0, 64 x 4096 x 4096 10.0 / 8.0 (left); groups: 16 rows of 16 groups,
 //   256 x 3360 4.3 / 9.9, 58 of 7, 1152 x 992 4.8 / 7.0, 64 of 32, 2048 x 4096
-//   33.4 / 25.6 (left).  A group of more than 32 rows takes two turns: 16 + 48 rows, 512
-//   x 4096 10.5 / 8.8, 9 + 23 rows 6.4 / 8.6.
+//   33.4 / 25.6 (left).
+// How even the groups' loads are is not known here.  A group of more than 16 f rows has
+// further workgroups: 192 rows over 8 groups of 512 x 7168 take 9.1 / 11.1 with 24 rows
+// each, 13.8 / 11.3 with up to 44 and 10.5 / 11.3 with all in one; 512 over 64 of 128 x
+// 1024 4.2 / 6.4, 5.9 / 6.4 and 4.6 / 6.5.  The worst of 15 sizes with loads of four
+// kinds: 15.8 / 11.3.
 int row_fragments(int64_t count, int64_t M, int64_t N, int64_t K, const Sched& s) {
   if (s.tm != 0 || s.tn != 0 || s.split > (count ? 1u : 0u)) return 0;
   const int64_t per = count ? cdiv(M, count) : M;  // rows of a group, on average
   if (per > (count ? 24 : 64)) return 0;
-  // (a group may have more rows than the average: they are taken in turns)
   const int64_t f = count ? (per <= 8 ? 1 : 2) : M <= 16 ? 1 : M <= 32 ? 2 : 4;
   const int64_t tiles = cdiv(N, 16) * std::max<int64_t>(count, 1);
   return f * cdiv(K, kMx4Stage) <= 56 && f * tiles <= 2 * device_cu_count() ? (int)f : 0;
@@ -183,7 +186,8 @@ bst_status gemm(bst_dtype c, bool grouped, int32_t G, const int32_t* group_m, in
   a.cvec = vec_rows(C, ldc, 0, out_bytes(c)) && 256 * ldc * out_bytes(c) < kSpan;
   a.far = is_far(M, N * out_bytes(c), 4 * kFar);
   if (rows) {
-    const dim3 grid((uint32_t)(cdiv(N, 16) * (grouped ? G : 1))), block(512);
+    // behind each group's first rows: at most a part for every 16 `rows` of the rest
+    const dim3 grid((uint32_t)(cdiv(N, 16) * (grouped ? G + M / (16 * rows) : 1))), block(512);
     auto run = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, block, 0, (hipStream_t)stream, a);
       return launched(hipGetLastError(), "4-bit product");

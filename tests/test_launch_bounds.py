@@ -90,6 +90,15 @@ def forms(L):
                                p(P), i64(H), p(P), None)
 
 
+def few_rows(L):
+    """Grouped products whose first tile count is at most the rows kernel's: N, K, G, M as arguments."""
+    for a in sys.argv[3:]:
+        N, K, G, M = map(int, a.split(","))
+        ld, ls = i64((K + 31) // 32 * 16), i64((K + 127) // 128 * 4)
+        L.bst_grouped_gemm_mx4(BF16, i32(G), p(P), i64(M), i64(N), i64(K), p(P), ld, p(P), ls, p(P), ld, i64(0), p(P),
+                               ls, i64(0), p(P), i64(N), None, None)
+
+
 SWEEPS = dict(gradients=gradients, sorts=sorts, moves=moves, quants=quants, products=products)
 
 
@@ -97,7 +106,7 @@ def child(sweep, path):
     runtime = ctypes.CDLL(None)
     L = ctypes.CDLL(LIB)
     runtime.record_launches(path.encode())
-    dict(SWEEPS, forms=forms)[sweep](L)
+    dict(SWEEPS, forms=forms, few_rows=few_rows)[sweep](L)
     runtime.record_end()
 
 
@@ -176,6 +185,19 @@ def test_cases_of_every_gradient_form(recorder):
             assert tasks == "one" or k > 4
     got = [(re.search(r"I\w+?EE", n).group(0), g) for n, g, b in recorder[1]("forms", *args)]
     assert got == want
+
+
+def test_rows_of_one_group_find_workgroups(recorder):
+    """The kernel for a few rows a group does not know the groups' loads when it is launched: each group
+    has workgroups for its first 16 FM rows, and there are as many more as all rows in one group need."""
+    sizes = [(16, 7168, 256, 6144), (16, 1024, 256, 2048), (256, 4096, 16, 384), (128, 14336, 64, 512),
+             (512, 7168, 8, 192), (2048, 7168, 2, 48), (100, 64, 1, 24), (4096, 4096, 2, 16)]
+    got = recorder[1]("few_rows", *("%d,%d,%d,%d" % s for s in sizes))
+    assert len(got) == len(sizes)
+    for (N, K, G, M), (name, grid, _) in zip(sizes, got):
+        fm = int(re.search(r"mx4_rows_kernelILi(\d+)E", name).group(1))
+        assert grid >= -(-N // 16) * max(G, -(-M // (16 * fm))), (N, K, G, M, name, grid)
+        assert grid >= -(-N // 16) * (G + max(0, -(-M // (16 * fm)) - 1)), (N, K, G, M, name, grid)
 
 
 if __name__ == "__main__":
