@@ -891,8 +891,8 @@ def phases(args, torch, np, I, gpu):
 def wg_times(args, torch, np, I, gpu):
     """Per-workgroup life of one launch (after 0.1 s of warm-up launches), from the production
     kernels' clock record (bst_set_clock_record: the 100 MHz reference counter at each
-    workgroup's start and end): the spread of the end times, their maximum per XCD (workgroup w
-    runs on XCD w mod 8), and the time by which all but the last 1% / 10% had ended.  One JSON
+    workgroup's start and end): the spread of the end times, their maximum per XCD (workgroups w of
+    one w mod 8 share an XCD), and the time by which all but the last 1% / 10% had ended.  One JSON
     line per (workload, schedule).  It shows how evenly a schedule spreads the units."""
     import block_swizzle_tile_amd as bst
 
